@@ -17,7 +17,7 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhstu.so")
 
-HSTU_BF16, HSTU_FP32 = 0, 1
+HSTU_BF16, HSTU_FP32, HSTU_FP16 = 0, 1, 2
 STATUS_NAMES = {0: "HSTU_OK", 1: "HSTU_ERR_INVALID_ARG", 2: "HSTU_ERR_UNSUPPORTED",
                 3: "HSTU_ERR_WORKSPACE", 4: "HSTU_ERR_CUDA", 5: "HSTU_ERR_BAD_OFFSETS",
                 6: "HSTU_ERR_TIMEOUT", 7: "HSTU_ERR_BAD_TIMESTAMPS", 8: "HSTU_ERR_BAD_IDS"}
@@ -26,6 +26,10 @@ STATUS_NAMES = {0: "HSTU_OK", 1: "HSTU_ERR_INVALID_ARG", 2: "HSTU_ERR_UNSUPPORTE
 EXPORTED = ["hstu_workspace_size", "hstu_layer_fwd", "hstu_stack_fwd", "hstu_mfalcon_rank",
             "hstu_bwd_workspace_size", "hstu_layer_bwd", "hstu_stack_bwd",
             "hstu_layer_fwd_noalloc", "hstu_sl_embed_workspace_size", "hstu_sl_embed",
+            "hstu_sl_embed_ids", "hstu_embed_workspace_size", "hstu_embed_fwd",
+            "hstu_embed_bwd_workspace_size", "hstu_embed_bwd", "hstu_embed_bwd_rows",
+            "hstu_grad_norm_workspace_size", "hstu_grad_norm", "hstu_adamw_workspace_size",
+            "hstu_adamw_step",
             "hstu_sl_keep_count", "hstu_bf16_to_f16", "hstu_retrieval_workspace_size",
             "hstu_retrieval_topk", "hstu_retrieval_fallback_taken",
             "hstu_transformer_workspace_size",
@@ -70,6 +74,26 @@ class LayerGrads(ctypes.Structure):
 class TransformerWeights(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in ("ln1_gamma", "ln1_beta", "W_qkv", "W_o", "ln2_gamma",
                                                "ln2_beta", "W_1", "b_1", "W_2", "b_2")]
+
+
+class AdamWTensor(ctypes.Structure):
+    """hstu_adamw_tensor."""
+    _fields_ = [("n", ctypes.c_int64), ("row_len", ctypes.c_int64), ("max_rows", ctypes.c_int64),
+                ("row_ids", ctypes.c_void_p), ("n_rows", ctypes.c_void_p),
+                ("grad", ctypes.c_void_p), ("param", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("copy_f16", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("weight_decay", ctypes.c_double),
+                ("grad_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32)]
+
+
+class AdamWArgs(ctypes.Structure):
+    """hstu_adamw_args."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("step_dev", ctypes.c_void_p),
+                ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p),
+                ("seed", ctypes.c_uint64)]
 
 
 _lib = None
@@ -126,6 +150,29 @@ def lib() -> ctypes.CDLL:
     L.hstu_sl_embed.argtypes = [i64, i64, i64, vp, vp, vp, ctypes.c_uint64, vp, i64, vp, i64, i32,
                                 vp, vp, vp, vp, sz, vp]
     L.hstu_sl_embed.restype = i32
+    L.hstu_sl_embed_ids.argtypes = [i64, i64, i64, vp, vp, vp, ctypes.c_uint64, vp, i64, vp, i64,
+                                    i32, vp, vp, vp, vp, vp, sz, vp]
+    L.hstu_sl_embed_ids.restype = i32
+    f32, pt = ctypes.c_float, ctypes.POINTER(AdamWTensor)
+    for name in ("hstu_embed_workspace_size", "hstu_grad_norm_workspace_size",
+                 "hstu_adamw_workspace_size"):
+        getattr(L, name).argtypes = []
+        getattr(L, name).restype = sz
+    L.hstu_embed_fwd.argtypes = [i64, vp, vp, i32, i64, i32, i64, i64, f32, vp, i32, i64, vp, sz,
+                                 vp]
+    L.hstu_embed_fwd.restype = i32
+    L.hstu_embed_bwd_workspace_size.argtypes = [i64, i64, i32]
+    L.hstu_embed_bwd_workspace_size.restype = sz
+    L.hstu_embed_bwd.argtypes = [i64, vp, vp, i32, i64, i64, i32, i64, f32, i32, vp, i32, i64, vp,
+                                 sz, vp]
+    L.hstu_embed_bwd.restype = i32
+    L.hstu_embed_bwd_rows.argtypes = [i64, vp, vp, i32, i64, i64, i32, i64, f32, vp, vp, i32, i64,
+                                      vp, vp, sz, vp]
+    L.hstu_embed_bwd_rows.restype = i32
+    L.hstu_grad_norm.argtypes = [pt, i32, ctypes.c_double, vp, vp, sz, vp]
+    L.hstu_grad_norm.restype = i32
+    L.hstu_adamw_step.argtypes = [ctypes.POINTER(AdamWArgs), pt, i32, vp, sz, vp]
+    L.hstu_adamw_step.restype = i32
     L.hstu_read_status.argtypes = [vp, sz, vp]
     L.hstu_read_status.restype = i32
     L.hstu_debug_offsets.argtypes = [pdesc, i64, i64, i64, ctypes.POINTER(sz),
@@ -334,6 +381,262 @@ def hstu_sl_embed(B, raw_total, max_raw_len, raw_offsets, raw_ids, raw_timestamp
                                _ptr(out_timestamps), _ptr(workspace), _nbytes(workspace),
                                _stream(stream)),
            "hstu_sl_embed")
+
+
+def hstu_sl_embed_ids(B, raw_total, max_raw_len, raw_offsets, raw_ids, raw_timestamps, seed,
+                      content_table, action_table, out_offsets, out_X, out_timestamps, out_ids,
+                      workspace, stream=None) -> None:
+    """hstu_sl_embed that also writes each kept token's row in the two tables
+    taken as one (see include/hstu.h)."""
+    _check(lib().hstu_sl_embed_ids(B, raw_total, max_raw_len, _ptr(raw_offsets), _ptr(raw_ids),
+                                   _ptr(raw_timestamps), int(seed) & ((1 << 64) - 1),
+                                   _ptr(content_table), int(content_table.shape[0]),
+                                   _ptr(action_table), int(action_table.shape[0]),
+                                   int(content_table.shape[1]), _ptr(out_offsets), _ptr(out_X),
+                                   _ptr(out_timestamps), _ptr(out_ids), _ptr(workspace),
+                                   _nbytes(workspace), _stream(stream)),
+           "hstu_sl_embed_ids")
+
+
+# ------------------------------------------------------ embedding and optimizer
+_DTYPES = None
+
+
+def _dtype(t, where: str) -> int:
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.bfloat16: HSTU_BF16, torch.float32: HSTU_FP32, torch.float16: HSTU_FP16}
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise HstuError(2, f"{where}: {t.dtype} tensor")
+    return code
+
+
+def _need(ok: bool, where: str, what: str) -> None:
+    if not ok:
+        raise HstuError(1, f"{where}: {what}")
+
+
+def _here(where: str, *tensors) -> None:
+    """Every tensor is on the current CUDA device (kernels are launched there)."""
+    import torch
+    for t in tensors:
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            raise HstuError(1, f"{where}: a tensor on {t.device}, not on the current CUDA device")
+
+
+def _rows(t, where: str, name: str) -> int:
+    """Row stride of a matrix whose rows are contiguous."""
+    _need(t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1), where,
+          f"{name}: rows of a matrix, contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(int(t.shape[1]), t.stride(0))
+
+
+def _i64(t, where: str, name: str) -> None:
+    import torch
+    _need(t.dtype == torch.int64 and t.is_contiguous(), where, f"{name}: a contiguous int64 tensor")
+
+
+def hstu_embed_workspace_size() -> int:
+    return int(lib().hstu_embed_workspace_size())
+
+
+def hstu_embed_fwd(ids, table, out, workspace, scale: float = 1.0, pad_id: int = -1,
+                   stream=None) -> None:
+    """out[t] = scale * table[ids[t]] (see include/hstu.h).  ids: int64 [T];
+    table [R, d] and out [T, d]: bf16, fp16 or fp32, rows contiguous."""
+    w = "hstu_embed_fwd"
+    _here(w, ids, table, out, workspace)
+    _i64(ids, w, "ids")
+    ldt, ldo = _rows(table, w, "table"), _rows(out, w, "out")
+    _need(out.shape[0] == ids.numel() and out.shape[1] == table.shape[1], w,
+          "out: [ids, table's columns]")
+    _check(lib().hstu_embed_fwd(ids.numel(), _ptr(ids), _ptr(table), _dtype(table, w),
+                                table.shape[0], table.shape[1], ldt, int(pad_id), float(scale),
+                                _ptr(out), _dtype(out, w), ldo, _ptr(workspace),
+                                _nbytes(workspace), _stream(stream)), w)
+
+
+def hstu_embed_bwd_workspace_size(n_tokens: int, n_rows: int, d: int) -> int:
+    n = int(lib().hstu_embed_bwd_workspace_size(n_tokens, n_rows, d))
+    if n == 0:
+        raise HstuError(1, "hstu_embed_bwd_workspace_size")
+    return n
+
+
+def hstu_embed_bwd(ids, dY, dE, workspace, scale: float = 1.0, pad_id: int = -1,
+                   accumulate: bool = False, stream=None) -> None:
+    """dE[r] = scale * sum of dY[t] over the tokens of row r, every row of the
+    table's gradient written, or added into it (see include/hstu.h)."""
+    w = "hstu_embed_bwd"
+    _here(w, ids, dY, dE, workspace)
+    _i64(ids, w, "ids")
+    ldy, lde = _rows(dY, w, "dY"), _rows(dE, w, "dE")
+    _need(dY.shape[0] == ids.numel() and dE.shape[1] == dY.shape[1], w, "dY: [ids, dE's columns]")
+    _check(lib().hstu_embed_bwd(ids.numel(), _ptr(ids), _ptr(dY), _dtype(dY, w), ldy, dE.shape[0],
+                                dE.shape[1], int(pad_id), float(scale), 1 if accumulate else 0,
+                                _ptr(dE), _dtype(dE, w), lde, _ptr(workspace), _nbytes(workspace),
+                                _stream(stream)), w)
+
+
+def hstu_embed_bwd_rows(ids, dY, n_rows: int, row_ids, rows, n_unique, workspace,
+                        scale: float = 1.0, pad_id: int = -1, stream=None) -> None:
+    """The touched rows of that gradient only: row_ids (int64, ascending), rows
+    and their number n_unique (int64 [1]); row_ids and rows hold min(ids,
+    n_rows) entries (see include/hstu.h)."""
+    w = "hstu_embed_bwd_rows"
+    _here(w, ids, dY, row_ids, rows, n_unique, workspace)
+    for t, name in ((ids, "ids"), (row_ids, "row_ids"), (n_unique, "n_unique")):
+        _i64(t, w, name)
+    ldy, ldr = _rows(dY, w, "dY"), _rows(rows, w, "rows")
+    cap = min(ids.numel(), int(n_rows))
+    _need(dY.shape[0] == ids.numel() and rows.shape[1] == dY.shape[1], w, "dY: [ids, rows' columns]")
+    _need(row_ids.numel() >= cap and rows.shape[0] >= cap and n_unique.numel() >= 1, w,
+          "row_ids, rows: min(ids, n_rows) entries")
+    _check(lib().hstu_embed_bwd_rows(ids.numel(), _ptr(ids), _ptr(dY), _dtype(dY, w), ldy,
+                                     int(n_rows), dY.shape[1], int(pad_id), float(scale),
+                                     _ptr(row_ids), _ptr(rows), _dtype(rows, w), ldr,
+                                     _ptr(n_unique), _ptr(workspace), _nbytes(workspace),
+                                     _stream(stream)), w)
+
+
+class GradTensors:
+    """A list of gradients laid out once for hstu_grad_norm: dicts with "grad"
+    (contiguous, bf16, fp16 or fp32) and, where only the first rows of it count,
+    "n_rows" (int64 [1] on the device)."""
+
+    def __init__(self, tensors: Sequence[Dict[str, object]]):
+        self.tensors = [dict(t) for t in tensors]  # keeps the memory alive
+        self.n = len(self.tensors)
+        self.array = (AdamWTensor * max(1, self.n))()
+        self.device = None
+        for c, t in zip(self.array, self.tensors):
+            self._fill(c, t)
+
+    def _take(self, t, name: str):
+        w = type(self).__name__
+        _need(t.is_contiguous() and t.is_cuda, w, f"{name}: a contiguous device tensor")
+        if self.device is None:
+            self.device = t.get_device()
+        _need(t.get_device() == self.device, w, f"{name}: on another device than the rest")
+        return _ptr(t)
+
+    def _fill(self, c, t) -> None:
+        w = type(self).__name__
+        g = t["grad"]
+        c.grad, c.grad_dtype, c.n = self._take(g, "grad"), _dtype(g, w), g.numel()
+        if t.get("n_rows") is not None:
+            _need(g.dim() == 2, w, "grad with n_rows: a matrix")
+            _i64(t["n_rows"], w, "n_rows")
+            c.n_rows = self._take(t["n_rows"], "n_rows")
+            c.max_rows, c.row_len = g.shape
+
+
+class AdamWTensors(GradTensors):
+    """A list of tensors laid out once for hstu_adamw_step (and hstu_grad_norm):
+    dicts with "param", "grad", "m", "v"; optional "master" (fp32), "copy_f16"
+    (fp16), "weight_decay"; with 8-bit states "m" and "v" are uint8 or
+    float8_e4m3fn and "m_scale", "v_scale" uint8 (state_scales() of the
+    parameter); for a table with a row gradient "row_ids" and "n_rows"."""
+
+    def _fill(self, c, t) -> None:
+        import torch
+        super()._fill(c, t)
+        w = type(self).__name__
+        p, g, m, v = (t[k] for k in ("param", "grad", "m", "v"))
+        sparse = t.get("row_ids") is not None
+        _need(sparse == (t.get("n_rows") is not None), w, "row_ids and n_rows come together")
+        if sparse:
+            _i64(t["row_ids"], w, "row_ids")
+            _need(p.dim() == 2 and g.shape[1] == p.shape[1], w, "grad: rows of param")
+            c.row_ids = self._take(t["row_ids"], "row_ids")
+            c.max_rows = min(g.shape[0], t["row_ids"].numel())
+        else:
+            _need(g.numel() == p.numel(), w, "grad: the size of param")
+        c.n = p.numel()
+        c.param, c.param_dtype = self._take(p, "param"), _dtype(p, w)
+        for k, dt in (("master", torch.float32), ("copy_f16", torch.float16)):
+            if t.get(k) is not None:
+                _need(t[k].dtype == dt and t[k].numel() == p.numel(), w, f"{k}: {dt}, as param")
+                setattr(c, k, self._take(t[k], k))
+        _need(m.dtype == v.dtype and m.numel() == v.numel() == p.numel(), w, "m, v: as param")
+        c.m, c.v = self._take(m, "m"), self._take(v, "v")
+        _need(m.dtype in (torch.float32, torch.uint8, torch.float8_e4m3fn), w,
+              "m, v: fp32, or uint8 or float8_e4m3fn codes")
+        c.state_bits = 32 if m.dtype == torch.float32 else 8
+        if c.state_bits == 8:
+            n = state_scales(p.shape if sparse else (p.numel(),))
+            for k in ("m_scale", "v_scale"):
+                _need(t.get(k) is not None and t[k].element_size() == 1 and t[k].numel() == n, w,
+                      f"{k}: {n} bytes")
+                setattr(c, k, self._take(t[k], k))
+        c.weight_decay = float(t.get("weight_decay", 0.0))
+
+
+def state_scales(shape) -> int:
+    """Number of scale bytes of 8-bit states: one per 256 elements of a dense
+    tensor (shape (n,)), or of each row of a table (shape (rows, d))."""
+    n = 1
+    for s in shape[:-1]:
+        n *= int(s)
+    return n * (-(-int(shape[-1]) // 256))
+
+
+def hstu_grad_norm_workspace_size() -> int:
+    return int(lib().hstu_grad_norm_workspace_size())
+
+
+def hstu_grad_norm(tensors: GradTensors, max_norm: float, out, workspace, stream=None) -> None:
+    """out (fp32 [2]): the norm over all gradients, and the factor that clips it
+    to max_norm (NaN if the norm is not finite); see include/hstu.h."""
+    import torch
+    w = "hstu_grad_norm"
+    _here(w, out, workspace)
+    _need(tensors.device is None or tensors.device == out.get_device(), w,
+          "the tensors are on another device")
+    _need(out.dtype == torch.float32 and out.is_contiguous() and out.numel() >= 2, w,
+          "out: fp32 [2]")
+    _check(lib().hstu_grad_norm(tensors.array, tensors.n, float(max_norm), _ptr(out),
+                                _ptr(workspace), _nbytes(workspace), _stream(stream)), w)
+
+
+def hstu_adamw_workspace_size() -> int:
+    return int(lib().hstu_adamw_workspace_size())
+
+
+def hstu_adamw_step(tensors: AdamWTensors, workspace, lr, step, beta1: float = 0.9,
+                    beta2: float = 0.999, eps: float = 1e-8, grad_scale=None, seed: int = 0,
+                    stream=None) -> None:
+    """One AdamW step of every tensor of the list (see include/hstu.h).  `lr`
+    and `step` are numbers, or device tensors (fp32 [1], int64 [1]) read by the
+    kernel; grad_scale: fp32 [1] on the device."""
+    import torch
+    w = "hstu_adamw_step"
+    _need(isinstance(tensors, AdamWTensors), w, "tensors: an AdamWTensors list")
+    _here(w, workspace)
+    _need(tensors.device is None or tensors.device == workspace.get_device(), w,
+          "the tensors are on another device")
+    a = AdamWArgs(0.0, beta1, beta2, eps, 1, None, None, None, int(seed) & ((1 << 64) - 1))
+    if isinstance(lr, torch.Tensor):
+        _here(w, lr)
+        _need(lr.dtype == torch.float32 and lr.numel() == 1, w, "lr: fp32 [1]")
+        a.lr_dev = _ptr(lr)
+    else:
+        a.lr = lr
+    if isinstance(step, torch.Tensor):
+        _here(w, step)
+        _need(step.dtype == torch.int64 and step.numel() == 1, w, "step: int64 [1]")
+        a.step_dev = _ptr(step)
+    else:
+        a.step = step
+    if grad_scale is not None:
+        _here(w, grad_scale)
+        _need(grad_scale.dtype == torch.float32 and grad_scale.numel() == 1, w,
+              "grad_scale: fp32 [1]")
+        a.grad_scale = _ptr(grad_scale)
+    _check(lib().hstu_adamw_step(ctypes.byref(a), tensors.array, tensors.n, _ptr(workspace),
+                                 _nbytes(workspace), _stream(stream)), w)
 
 
 def hstu_stack_fwd(desc, n_layers, weights, B, total_tokens, max_len, offsets, X, timestamps,

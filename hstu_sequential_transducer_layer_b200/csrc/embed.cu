@@ -1,0 +1,911 @@
+// embed.cu — embedding lookup with scaling, and its gradient by sorted tokens.
+//
+// Forward: Y[t] = scale * E[ids[t]].  Backward: dE[r] = scale * the sum over
+// the tokens t with ids[t] = r of dY[t], in fp32, the same bit for bit on
+// every run: the tokens are sorted by (id, t) with a stable radix sort, so
+// that each touched row is one contiguous segment of the sorted order, and
+// the segments are summed in that order.
+//
+// A user whose tokens are half actions gives segments of very different
+// length (an action row holds thousands of tokens, most content rows one or
+// two), so the sum is cut by sorted position, not by row: a block takes
+// kRun = 128 consecutive positions and 256 columns, each of its 8 warps 16
+// positions.  A segment inside one warp's positions is written at once; the
+// parts of a segment that passes a warp's border are joined through shared
+// memory, and the parts of one that passes a block's border through the
+// workspace (at most two partial rows per block), by k_embed_join.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "ptx.cuh"
+
+namespace hstu {
+namespace {
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortItems = 8;
+constexpr int kSortTile = kSortThreads * kSortItems;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 10;  // at most; bins of one pass
+constexpr int kMaxBins = 1 << kDigitBits;
+
+constexpr int kRunWarps = 8;
+constexpr int kRunTokens = 16;                     // sorted positions of one warp
+constexpr int kRun = kRunWarps * kRunTokens;       // of one block
+constexpr int kColumns = 256;                      // columns of one block, 8 per lane
+
+constexpr int64_t kMaxTokens = 0x7fffffffll - kSortTile;
+constexpr int64_t kMaxRows = 0x7ffffffell;
+
+// ---------------------------------------------------------------- elements
+// 8 elements of a row as fp32.  Vector form: the lane's 8 consecutive ones,
+// 16 bytes (32 for fp32) at an aligned address.
+template <int DT>
+struct Raw8 {
+  uint4 a;
+};
+template <>
+struct Raw8<HSTU_FP32> {
+  uint4 a, b;
+};
+DEVI void load8(Raw8<HSTU_BF16>& r, const void* p, int64_t e) {
+  r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + e));
+}
+DEVI void load8(Raw8<HSTU_FP16>& r, const void* p, int64_t e) {
+  r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(p) + e));
+}
+DEVI void load8(Raw8<HSTU_FP32>& r, const void* p, int64_t e) {
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + e);
+  r.a = __ldg(q);
+  r.b = __ldg(q + 1);
+}
+DEVI void widen(const Raw8<HSTU_BF16>& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+DEVI void widen(const Raw8<HSTU_FP16>& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = x.x;
+    f[2 * i + 1] = x.y;
+  }
+}
+DEVI void widen(const Raw8<HSTU_FP32>& r, float (&f)[8]) {
+  f[0] = __uint_as_float(r.a.x);
+  f[1] = __uint_as_float(r.a.y);
+  f[2] = __uint_as_float(r.a.z);
+  f[3] = __uint_as_float(r.a.w);
+  f[4] = __uint_as_float(r.b.x);
+  f[5] = __uint_as_float(r.b.y);
+  f[6] = __uint_as_float(r.b.z);
+  f[7] = __uint_as_float(r.b.w);
+}
+template <int DT>
+DEVI float load1(const void* p, int64_t e) {
+  if (DT == HSTU_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[e]);
+  if (DT == HSTU_FP16) return __half2float(static_cast<const __half*>(p)[e]);
+  return static_cast<const float*>(p)[e];
+}
+DEVI float load1_dyn(int dt, const void* p, int64_t e) {
+  return dt == HSTU_BF16 ? load1<HSTU_BF16>(p, e)
+                         : dt == HSTU_FP16 ? load1<HSTU_FP16>(p, e) : load1<HSTU_FP32>(p, e);
+}
+// The type of what is written is the same for the whole launch: a branch per
+// store instead of a kernel per pair of types.
+DEVI void store1(int dt, void* p, int64_t e, float x) {
+  if (dt == HSTU_BF16)
+    static_cast<__nv_bfloat16*>(p)[e] = __float2bfloat16_rn(x);
+  else if (dt == HSTU_FP16)
+    static_cast<__half*>(p)[e] = __float2half_rn(x);
+  else
+    static_cast<float*>(p)[e] = x;
+}
+DEVI void store8(int dt, void* p, int64_t e, const float (&f)[8]) {
+  if (dt == HSTU_FP32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + e);
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (dt == HSTU_BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + e) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------- lookup
+struct LookupArgs {
+  const int64_t* ids;
+  const void* table;
+  void* out;
+  int* status;
+  int64_t T, R, ldt, ldo, pad;
+  float scale;
+  int out_dt, d, cols;  // cols: threads along a row; blockDim.x = cols * rows per block
+  int check;            // block 0 only validates the ids; else every block reports its own
+};
+
+constexpr int kLookupUnroll = 4;
+constexpr int64_t kCheckMax = 65536;
+
+// Y[t] = scale * E[ids[t]].  Bandwidth-bound; a thread keeps one column
+// group of 8 elements (1 where a row is not a multiple of 8) and walks the
+// tokens, 4 loads in flight, so that no index is divided inside the loop.
+// A thread of one block cannot clear the status word before another one sets
+// it, so up to kCheckMax tokens block 0 copies nothing and validates all ids
+// itself (its 8 bytes per token are read while the others copy); beyond that
+// the word is cleared by a memset before the launch.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) k_embed_lookup(const LookupArgs a) {
+  if (a.check && blockIdx.x == 0) {
+    bool bad = false;
+    for (int64_t t = threadIdx.x; t < a.T; t += blockDim.x) {
+      const int64_t id = a.ids[t];
+      bad |= id != a.pad && (id < 0 || id >= a.R);
+    }
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *a.status = any ? HSTU_ERR_BAD_IDS : HSTU_OK;
+    return;
+  }
+  const int rows = blockDim.x / a.cols;
+  const int c0 = threadIdx.x % a.cols, r0 = threadIdx.x / a.cols;
+  const int64_t block = (int64_t)blockIdx.x - a.check, blocks = (int64_t)gridDim.x - a.check;
+  const int n_cols = VEC ? a.d / 8 : a.d;
+  for (int64_t t0 = block * rows * kLookupUnroll + r0; t0 < a.T;
+       t0 += blocks * rows * kLookupUnroll) {
+    int64_t id[kLookupUnroll];
+#pragma unroll
+    for (int u = 0; u < kLookupUnroll; ++u) {
+      const int64_t t = t0 + (int64_t)u * rows;
+      id[u] = t < a.T ? a.ids[t] : -1;
+      const bool in = id[u] >= 0 && id[u] < a.R;
+      if (!a.check && t < a.T && !in && id[u] != a.pad && c0 == 0)
+        atomicCAS(a.status, HSTU_OK, HSTU_ERR_BAD_IDS);
+      if (!in || id[u] == a.pad) id[u] = -1;
+    }
+    for (int c = c0; c < n_cols; c += a.cols) {
+      if (VEC) {
+        Raw8<DT> r[kLookupUnroll];
+#pragma unroll
+        for (int u = 0; u < kLookupUnroll; ++u) {
+          r[u] = Raw8<DT>{};
+          if (id[u] >= 0) load8(r[u], a.table, id[u] * a.ldt + 8 * (int64_t)c);
+        }
+#pragma unroll
+        for (int u = 0; u < kLookupUnroll; ++u) {
+          const int64_t t = t0 + (int64_t)u * rows;
+          float f[8];
+          widen(r[u], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = id[u] >= 0 ? f[j] * a.scale : 0.f;
+          if (t < a.T) store8(a.out_dt, a.out, t * a.ldo + 8 * (int64_t)c, f);
+        }
+      } else {
+        float f[kLookupUnroll];
+#pragma unroll
+        for (int u = 0; u < kLookupUnroll; ++u)
+          f[u] = id[u] >= 0 ? load1<DT>(a.table, id[u] * a.ldt + c) * a.scale : 0.f;
+#pragma unroll
+        for (int u = 0; u < kLookupUnroll; ++u) {
+          const int64_t t = t0 + (int64_t)u * rows;
+          if (t < a.T) store1(a.out_dt, a.out, t * a.ldo + c, f[u]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sort
+// Header of the gradient's workspace.
+struct SortHead {
+  int32_t status;
+  int32_t live;   // sorted positions that hold a token of a table row
+  int32_t segs;   // touched rows
+};
+
+struct SortArgs {
+  const int64_t* ids;
+  int64_t pad;
+  uint32_t n_rows;         // also the key of tokens that are dropped (pad, bad id)
+  int T, tiles, passes, digit;
+  uint32_t* key[2];        // ping-pong; keys of pass p in key[p & 1]
+  uint32_t* val[2];        // token numbers (pass 0 reads none: position = token)
+  uint32_t* hist;          // [tiles, bins] counts, then exclusive over tiles; [bins] totals behind
+  int32_t* bad;            // per tile: an id outside the table was seen
+  int32_t* heads;          // per tile: touched rows that start in it
+  uint32_t* rank;          // per sorted position: its segment
+  uint32_t* seg_start;     // per segment: its first sorted position
+  int64_t* row_ids;        // compact form: the touched rows (else null)
+  int64_t* n_unique;       // compact form: their number (else null)
+  SortHead* head;
+};
+
+DEVI uint32_t token_key(const SortArgs& a, int64_t id, bool* bad) {
+  const bool in = id >= 0 && id < (int64_t)a.n_rows;
+  *bad = !in && id != a.pad;
+  return in && id != a.pad ? (uint32_t)id : a.n_rows;
+}
+
+// Counts of one pass's digits in each tile; the first pass also turns ids
+// into keys.
+__global__ void __launch_bounds__(kSortThreads) k_sort_count(const SortArgs a, int pass) {
+  __shared__ uint32_t s_hist[kMaxBins];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int bins = 1 << a.digit, shift = pass * a.digit;
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) s_hist[b] = 0;
+  __syncthreads();
+  const int base = blockIdx.x * kSortTile;
+  bool any_bad = false;
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = base + k * kSortThreads + threadIdx.x;
+    if (i < a.T) {
+      uint32_t key;
+      if (pass == 0) {
+        bool bad;
+        key = token_key(a, a.ids[i], &bad);
+        any_bad |= bad;
+        a.key[0][i] = key;
+      } else {
+        key = a.key[pass & 1][i];
+      }
+      atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
+    }
+  }
+  const int tile_bad = __syncthreads_or(any_bad);
+  if (pass == 0 && threadIdx.x == 0) a.bad[blockIdx.x] = tile_bad;
+  for (int b = threadIdx.x; b < bins; b += kSortThreads)
+    a.hist[(size_t)blockIdx.x * bins + b] = s_hist[b];
+}
+
+// Counts -> exclusive sums over the tiles, per digit, and the digits' totals.
+__global__ void k_sort_scan(const SortArgs a, int pass) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int bins = 1 << a.digit;
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b < bins) {
+    uint32_t sum = 0;
+    uint32_t* col = a.hist + b;
+#pragma unroll 8
+    for (int t = 0; t < a.tiles; ++t) {
+      const uint32_t n = col[(size_t)t * bins];
+      col[(size_t)t * bins] = sum;
+      sum += n;
+    }
+    col[(size_t)a.tiles * bins] = sum;
+  }
+  if (pass == 0 && blockIdx.x == 0) {
+    bool bad = false;
+    for (int t = threadIdx.x; t < a.tiles; t += blockDim.x) bad |= a.bad[t] != 0;
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) a.head->status = any ? HSTU_ERR_BAD_IDS : HSTU_OK;
+  }
+}
+
+// Ranks a tile's items among those of the same digit, in tile order: each
+// warp counts its own 256 consecutive items (equal digits of one 32-item step
+// found by match), then the warps' counts are summed up per digit.  On return
+// hist[w][b] is the number of items of digit b in warps before w, and rank[k]
+// this thread's item's number inside its warp.
+DEVI void rank_tile(const uint32_t (&digit)[kSortItems], const bool (&in)[kSortItems], int bins,
+                    uint16_t* hist, uint32_t (&rank)[kSortItems]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kSortWarps * bins / 2; i += kSortThreads)
+    reinterpret_cast<uint32_t*>(hist)[i] = 0;
+  __syncthreads();
+  uint16_t* mine = hist + warp * bins;
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const uint32_t d = in[k] ? digit[k] : 0xffffffffu;
+    const uint32_t peers = __match_any_sync(0xffffffffu, d);
+    const uint32_t before = in[k] ? mine[d] : 0;
+    rank[k] = before + __popc(peers & ((1u << lane) - 1));
+    __syncwarp();
+    if (in[k] && lane == __ffs(peers) - 1) mine[d] = (uint16_t)(before + __popc(peers));
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+    uint32_t sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t n = hist[w * bins + b];
+      hist[w * bins + b] = (uint16_t)sum;
+      sum += n;
+    }
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const SortArgs a, int pass) {
+  extern __shared__ uint16_t s_warp_hist[];
+  __shared__ uint32_t s_base[kMaxBins];
+  __shared__ int s_scan[kSortWarps];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int bins = 1 << a.digit, shift = pass * a.digit;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  {  // first position of each digit of this tile (bins <= threads)
+    const int b = threadIdx.x;
+    const int total = b < bins ? (int)a.hist[(size_t)a.tiles * bins + b] : 0;
+    int all;
+    const int base = block_excl_scan<kSortThreads>(total, s_scan, &all);
+    if (b < bins) s_base[b] = base + a.hist[(size_t)blockIdx.x * bins + b];
+  }
+  uint32_t key[kSortItems], digit[kSortItems], rank[kSortItems];
+  bool in[kSortItems];
+  const int base = blockIdx.x * kSortTile + warp * (32 * kSortItems) + lane;
+  const uint32_t* src = a.key[pass & 1];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = base + k * 32;
+    in[k] = i < a.T;
+    key[k] = in[k] ? src[i] : 0;
+    digit[k] = (key[k] >> shift) & (bins - 1);
+  }
+  rank_tile(digit, in, bins, s_warp_hist, rank);
+  uint32_t* dst_key = a.key[(pass + 1) & 1];
+  uint32_t* dst_val = a.val[(pass + 1) & 1];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    if (!in[k]) continue;
+    const int i = base + k * 32;
+    const uint32_t to = s_base[digit[k]] + s_warp_hist[warp * bins + digit[k]] + rank[k];
+    dst_key[to] = key[k];
+    dst_val[to] = pass == 0 ? (uint32_t)i : a.val[pass & 1][i];
+  }
+}
+
+// Whether a segment starts at sorted position i; dropped tokens start none.
+DEVI bool seg_head(const uint32_t* key, uint32_t n_rows, int i) {
+  const uint32_t k = key[i];
+  return k < n_rows && (i == 0 || key[i - 1] != k);
+}
+
+__global__ void __launch_bounds__(kSortThreads) k_sort_heads(const SortArgs a) {
+  __shared__ int s_scan[kSortWarps];
+  grid_dep_launch();
+  grid_dep_wait();
+  const uint32_t* key = a.key[a.passes & 1];
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = blockIdx.x * kSortTile + k * kSortThreads + threadIdx.x;
+    n += i < a.T && seg_head(key, a.n_rows, i);
+  }
+  int all;
+  block_excl_scan<kSortThreads>(n, s_scan, &all);
+  if (threadIdx.x == 0) a.heads[blockIdx.x] = all;
+}
+
+// Segment number of every sorted position, each segment's start, the touched
+// rows and the counts.
+__global__ void __launch_bounds__(kSortThreads) k_sort_segments(const SortArgs a) {
+  __shared__ int s_scan[kSortWarps];
+  grid_dep_launch();
+  grid_dep_wait();
+  const uint32_t* key = a.key[a.passes & 1];
+  int before = 0;
+  for (int t = threadIdx.x; t < (int)blockIdx.x; t += kSortThreads) before += a.heads[t];
+  int run;
+  block_excl_scan<kSortThreads>(before, s_scan, &run);
+  const bool last_tile = blockIdx.x == gridDim.x - 1;
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = blockIdx.x * kSortTile + k * kSortThreads + threadIdx.x;
+    const bool valid = i < a.T && key[i] < a.n_rows;
+    const bool h = i < a.T && seg_head(key, a.n_rows, i);
+    int all;
+    const int pre = block_excl_scan<kSortThreads>(h, s_scan, &all);
+    if (valid) {
+      const int seg = run + pre + h - 1;
+      a.rank[i] = (uint32_t)seg;
+      if (h) {
+        a.seg_start[seg] = (uint32_t)i;
+        if (a.row_ids) a.row_ids[seg] = (int64_t)key[i];
+      }
+      if (i + 1 == a.T || key[i + 1] >= a.n_rows) a.head->live = i + 1;
+    }
+    if (i == 0 && !valid) a.head->live = 0;
+    run += all;
+  }
+  if (last_tile && threadIdx.x == 0) {
+    a.head->segs = run;
+    if (a.n_unique) *a.n_unique = run;
+  }
+}
+
+// ---------------------------------------------------------------- sums
+struct SumArgs {
+  const SortHead* head;
+  const uint32_t* key;
+  const uint32_t* val;
+  const uint32_t* rank;
+  const uint32_t* seg_start;
+  const void* dY;
+  void* out;
+  float* part;        // [runs, 2, ld_part]
+  int64_t ld_dy, ld_out;
+  float scale;
+  int d, ld_part, out_dt, compact, accumulate;
+};
+
+// Column (vector form: first of 8) of this lane, and the elements' stride.
+template <bool VEC>
+DEVI int lane_col(int lane, int j) {
+  return VEC ? 8 * lane + j : 32 * j + lane;
+}
+
+template <bool VEC>
+DEVI void write_row(const SumArgs& a, uint32_t key, uint32_t rank, int c0, int lane,
+                    const float (&acc)[8]) {
+  const int64_t at = (int64_t)(a.compact ? rank : key) * a.ld_out + c0;
+  if (VEC) {
+    if (c0 + 8 * lane >= a.d) return;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = acc[j] * a.scale;
+      if (a.accumulate) f[j] += load1_dyn(a.out_dt, a.out, at + 8 * lane + j);
+    }
+    store8(a.out_dt, a.out, at + 8 * lane, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = 32 * j + lane;
+      if (c0 + c < a.d) {
+        float f = acc[j] * a.scale;
+        if (a.accumulate) f += load1_dyn(a.out_dt, a.out, at + c);
+        store1(a.out_dt, a.out, at + c, f);
+      }
+    }
+  }
+}
+
+// Partial rows keep the lane's own order (8 floats per lane), in either form.
+DEVI void put8(float* p, int lane, const float (&f)[8]) {
+  float4* q = reinterpret_cast<float4*>(p + 8 * lane);
+  q[0] = make_float4(f[0], f[1], f[2], f[3]);
+  q[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+DEVI void add8(const float* p, int lane, float (&f)[8]) {
+  const float4* q = reinterpret_cast<const float4*>(p + 8 * lane);
+  const float4 x = q[0], y = q[1];
+  f[0] += x.x;
+  f[1] += x.y;
+  f[2] += x.z;
+  f[3] += x.w;
+  f[4] += y.x;
+  f[5] += y.y;
+  f[6] += y.z;
+  f[7] += y.w;
+}
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kRunWarps * 32) k_embed_sum(const SumArgs a) {
+  __shared__ float s_pre[kRunWarps][kColumns], s_post[kRunWarps][kColumns];
+  __shared__ int s_flags[kRunWarps];  // 1: pre holds a part, 2: it goes on past this warp
+  grid_dep_launch();
+  grid_dep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int live = a.head->live;
+  const int b0 = blockIdx.x * kRun;
+  if (b0 >= live) return;
+  const int c0 = blockIdx.y * kColumns;
+  const int p0 = b0 + warp * kRunTokens;
+  const int n = min(kRunTokens, live - p0);  // may be <= 0
+  // the warp's keys, tokens and segments, one position per lane; lane n holds the next
+  // position's key (n <= 16, so there is room)
+  uint32_t key = 0xffffffffu, val = 0, rank = 0, prev = 0xffffffffu;
+  if (n > 0) {
+    if (lane <= n && p0 + lane < live) key = a.key[p0 + lane];
+    if (lane < n) {
+      val = a.val[p0 + lane];
+      rank = a.rank[p0 + lane];
+    }
+    if (p0 > 0) prev = a.key[p0 - 1];
+  }
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  int flags = 0;
+  bool post = false;
+  uint32_t cur = 0, cur_rank = 0;
+  if (n > 0) {
+    cur = __shfl_sync(0xffffffffu, key, 0);
+    cur_rank = __shfl_sync(0xffffffffu, rank, 0);
+    bool open = cur == prev;  // the running segment began before this warp's positions
+    constexpr int kBatch = DT == HSTU_FP32 ? 4 : 8;
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float x[kBatch][8];
+      if (VEC) {
+        Raw8<DT> r[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          r[u] = Raw8<DT>{};
+          const int64_t t = __shfl_sync(0xffffffffu, val, (i0 + u) & 31);
+          if (i0 + u < n && c0 + 8 * lane < a.d) load8(r[u], a.dY, t * a.ld_dy + c0 + 8 * lane);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) widen(r[u], x[u]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int64_t t = __shfl_sync(0xffffffffu, val, (i0 + u) & 31);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int c = c0 + 32 * j + lane;
+            x[u][j] = i0 + u < n && c < a.d ? load1<DT>(a.dY, t * a.ld_dy + c) : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (i0 + u < n) {
+          const uint32_t k = __shfl_sync(0xffffffffu, key, i0 + u);
+          if (k != cur) {  // the running segment ends here
+            if (open) {
+              put8(s_pre[warp], lane, acc);
+              flags = 1;
+            } else {
+              write_row<VEC>(a, cur, cur_rank, c0, lane, acc);
+            }
+            open = false;
+            cur = k;
+            cur_rank = __shfl_sync(0xffffffffu, rank, i0 + u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] += x[u][j];
+        }
+      }
+    }
+    const bool on = __shfl_sync(0xffffffffu, key, n) == cur;  // goes on behind this warp
+    if (open) {
+      put8(s_pre[warp], lane, acc);
+      flags = on ? 3 : 1;
+    } else if (on) {
+      put8(s_post[warp], lane, acc);
+      post = true;
+    } else {
+      write_row<VEC>(a, cur, cur_rank, c0, lane, acc);
+    }
+  }
+  if (lane == 0) s_flags[warp] = flags;
+  __syncthreads();
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.ld_part + c0;
+  // the part that began before this block, and this warp's own segment that goes on
+  for (int which = 0; which < 2; ++which) {
+    if (which == 0 ? !(warp == 0 && (flags & 1)) : !post) continue;
+    int w = which == 0 ? 0 : warp;
+    const bool ends_here = which == 0 && !(flags & 2);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    add8(which == 0 ? s_pre[0] : s_post[warp], lane, acc);
+    bool done = ends_here;
+    while (!done && ++w < kRunWarps) {
+      add8(s_pre[w], lane, acc);
+      done = !(s_flags[w] & 2);
+    }
+    if (which == 0)
+      put8(part, lane, acc);
+    else if (done)
+      write_row<VEC>(a, cur, cur_rank, c0, lane, acc);
+    else
+      put8(part + a.ld_part, lane, acc);
+  }
+}
+
+// Joins the parts of a segment that starts in run `blockIdx.x` and goes on
+// behind it: this run's second part, then the first part of each later run
+// that it reaches, the runs split among the warps in order.
+constexpr int kJoinWarps = 16;
+template <bool VEC>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_embed_join(const SumArgs a) {
+  __shared__ float s_acc[kJoinWarps][kColumns];
+  grid_dep_wait();
+  const int live = a.head->live, segs = a.head->segs;
+  const int e = (int)min((int64_t)(blockIdx.x + 1) * kRun, (int64_t)live);
+  if (e >= live) return;
+  const uint32_t k = a.key[e - 1];
+  if (a.key[e] != k) return;
+  const uint32_t rank = a.rank[e - 1];
+  if ((int)a.seg_start[rank] < e - kRun) return;
+  const int end = (int)rank + 1 < segs ? (int)a.seg_start[rank + 1] : live;
+  const int first = blockIdx.x + 1, last = (end - 1) / kRun;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.y * kColumns;
+  const int per = (last - first + kJoinWarps) / kJoinWarps;
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  if (warp == 0)
+    add8(a.part + ((int64_t)blockIdx.x * 2 + 1) * a.ld_part + c0, lane, acc);
+  const int r1 = min(first + (warp + 1) * per, last + 1);
+#pragma unroll 4
+  for (int r = first + warp * per; r < r1; ++r)
+    add8(a.part + (int64_t)r * 2 * a.ld_part + c0, lane, acc);
+  put8(s_acc[warp], lane, acc);
+  __syncthreads();
+  if (warp != 0) return;
+  for (int w = 1; w < kJoinWarps; ++w) add8(s_acc[w], lane, acc);
+  write_row<VEC>(a, k, rank, c0, lane, acc);
+}
+
+// ---------------------------------------------------------------- host
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+bool dtype_ok(int32_t t) { return t == HSTU_BF16 || t == HSTU_FP32 || t == HSTU_FP16; }
+size_t dsize(int32_t t) { return t == HSTU_FP32 ? 4 : 2; }
+
+struct BwdLayout {
+  size_t head, key[2], val[2], hist, bad, heads, rank, seg_start, part, total;
+  int tiles, passes, digit, runs, ld_part;
+};
+
+bool bwd_layout(int64_t T, int64_t R, int32_t d, BwdLayout* L) {
+  if (T < 0 || T > kMaxTokens || R < 1 || R > kMaxRows || d < 1 || d > (1 << 20)) return false;
+  int bits = 1;
+  while (bits < 31 && ((int64_t)1 << bits) <= R) ++bits;  // keys 0 .. R (R: dropped)
+  L->passes = (bits + kDigitBits - 1) / kDigitBits;
+  L->digit = (bits + L->passes - 1) / L->passes;
+  L->tiles = (int)((T + kSortTile - 1) / kSortTile);
+  L->runs = (int)((T + kRun - 1) / kRun);
+  L->ld_part = (d + kColumns - 1) / kColumns * kColumns;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 255) & ~size_t(255);
+    return o;
+  };
+  L->head = take(256);
+  for (int i = 0; i < 2; ++i) {
+    L->key[i] = take((size_t)T * 4);
+    L->val[i] = take((size_t)T * 4);
+  }
+  L->hist = take(((size_t)L->tiles + 1) * 4 << L->digit);
+  L->bad = take((size_t)L->tiles * 4);
+  L->heads = take((size_t)L->tiles * 4);
+  L->rank = take((size_t)T * 4);
+  L->seg_start = take((size_t)T * 4);
+  L->part = take((size_t)L->runs * 2 * L->ld_part * 4);
+  L->total = off;
+  return true;
+}
+
+// Launches with programmatic stream serialization: the kernel may start while
+// its predecessor runs and waits for it (griddepcontrol.wait) before touching
+// anything.
+template <typename... P, typename... A>
+cudaError_t launch_dep(int id, void (*fn)(P...), dim3 grid, int threads, size_t smem,
+                       cudaStream_t s, bool dep, A... args) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = dep ? 1 : 0;
+  LaunchScope ls(id, s);
+  return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
+
+cudaError_t sort_tokens(const SortArgs& a, cudaStream_t s) {
+  const int bins = 1 << a.digit;
+  const size_t smem = (size_t)kSortWarps * bins * 2;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(k_sort_scatter), (int)smem);
+  for (int p = 0; p < a.passes && e == cudaSuccess; ++p) {
+    e = launch_dep(K_EMBED_SORT, k_sort_count, dim3(a.tiles), kSortThreads, 0, s, p > 0, a, p);
+    if (e == cudaSuccess)
+      e = launch_dep(K_EMBED_SORT, k_sort_scan, dim3((bins + 63) / 64), 64, 0, s, true, a, p);
+    if (e == cudaSuccess)
+      e = launch_dep(K_EMBED_SORT, k_sort_scatter, dim3(a.tiles), kSortThreads, smem, s, true, a, p);
+  }
+  if (e == cudaSuccess)
+    e = launch_dep(K_EMBED_SORT, k_sort_heads, dim3(a.tiles), kSortThreads, 0, s, true, a);
+  if (e == cudaSuccess)
+    e = launch_dep(K_EMBED_SORT, k_sort_segments, dim3(a.tiles), kSortThreads, 0, s, true, a);
+  return e;
+}
+
+template <int DT>
+cudaError_t sum_rows(const SumArgs& a, int runs, bool vec, cudaStream_t s) {
+  const dim3 grid((unsigned)runs, (unsigned)((a.d + kColumns - 1) / kColumns));
+  cudaError_t e = vec ? launch_dep(K_EMBED_SUM, k_embed_sum<DT, true>, grid, kRunWarps * 32, 0, s,
+                                   true, a)
+                      : launch_dep(K_EMBED_SUM, k_embed_sum<DT, false>, grid, kRunWarps * 32, 0, s,
+                                   true, a);
+  if (e != cudaSuccess) return e;
+  return vec ? launch_dep(K_EMBED_JOIN, k_embed_join<true>, grid, kJoinWarps * 32, 0, s, true, a)
+             : launch_dep(K_EMBED_JOIN, k_embed_join<false>, grid, kJoinWarps * 32, 0, s, true, a);
+}
+
+hstu_status cuda_status(cudaError_t e, const char* where) {
+  if (e == cudaSuccess) return HSTU_OK;
+  note_cuda_error(e, where);
+  return HSTU_ERR_CUDA;
+}
+
+hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_dt, int64_t ld_dy,
+                      int64_t R, int32_t d, int64_t pad, float scale, int accumulate, int compact,
+                      int64_t* row_ids, int64_t* n_unique, void* out, int32_t out_dt,
+                      int64_t ld_out, void* ws, size_t ws_bytes, cudaStream_t s) {
+  BwdLayout L;
+  if (!bwd_layout(T, R, d, &L)) return HSTU_ERR_INVALID_ARG;
+  if (!dtype_ok(dy_dt) || !dtype_ok(out_dt) || ld_dy < d || ld_out < d) return HSTU_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return HSTU_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return HSTU_ERR_INVALID_ARG;  // NaN or infinite
+  if (T > 0 && (!ids || !dY || !out)) return HSTU_ERR_INVALID_ARG;
+  if (compact && (!n_unique || (T > 0 && !row_ids))) return HSTU_ERR_INVALID_ARG;
+  if (!compact && !out) return HSTU_ERR_INVALID_ARG;
+  if (!al16(ids) || !al16(dY) || !al16(out) || !al16(row_ids) || !al16(n_unique))
+    return HSTU_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < L.total || !al256(ws)) return HSTU_ERR_WORKSPACE;
+  auto at = [&](size_t o) { return static_cast<uint8_t*>(ws) + o; };
+  SortHead* head = reinterpret_cast<SortHead*>(at(L.head));
+  if (!compact && !accumulate) {
+    const size_t row = (size_t)d * dsize(out_dt), pitch = (size_t)ld_out * dsize(out_dt);
+    const cudaError_t e = row == pitch ? cudaMemsetAsync(out, 0, (size_t)R * row, s)
+                                       : cudaMemset2DAsync(out, pitch, 0, row, (size_t)R, s);
+    if (e != cudaSuccess) return cuda_status(e, "embed_bwd: clearing the gradient");
+  }
+  if (T == 0) {
+    cudaError_t e = cudaMemsetAsync(head, 0, sizeof(SortHead), s);
+    if (e == cudaSuccess && compact) e = cudaMemsetAsync(n_unique, 0, 8, s);
+    return cuda_status(e, "embed_bwd: empty batch");
+  }
+  SortArgs q{};
+  q.ids = ids;
+  q.pad = pad;
+  q.n_rows = (uint32_t)R;
+  q.T = (int)T;
+  q.tiles = L.tiles;
+  q.passes = L.passes;
+  q.digit = L.digit;
+  for (int i = 0; i < 2; ++i) {
+    q.key[i] = reinterpret_cast<uint32_t*>(at(L.key[i]));
+    q.val[i] = reinterpret_cast<uint32_t*>(at(L.val[i]));
+  }
+  q.hist = reinterpret_cast<uint32_t*>(at(L.hist));
+  q.bad = reinterpret_cast<int32_t*>(at(L.bad));
+  q.heads = reinterpret_cast<int32_t*>(at(L.heads));
+  q.rank = reinterpret_cast<uint32_t*>(at(L.rank));
+  q.seg_start = reinterpret_cast<uint32_t*>(at(L.seg_start));
+  q.row_ids = compact ? row_ids : nullptr;
+  q.n_unique = compact ? n_unique : nullptr;
+  q.head = head;
+  cudaError_t e = sort_tokens(q, s);
+  if (e != cudaSuccess) return cuda_status(e, "embed_bwd: sort");
+  SumArgs a{};
+  a.head = head;
+  a.key = q.key[L.passes & 1];
+  a.val = q.val[L.passes & 1];
+  a.rank = q.rank;
+  a.seg_start = q.seg_start;
+  a.dY = dY;
+  a.out = out;
+  a.part = reinterpret_cast<float*>(at(L.part));
+  a.ld_dy = ld_dy;
+  a.ld_out = ld_out;
+  a.scale = scale;
+  a.d = d;
+  a.ld_part = L.ld_part;
+  a.out_dt = out_dt;
+  a.compact = compact;
+  a.accumulate = accumulate;
+  const bool vec = d % 8 == 0 && ld_dy % 8 == 0 && ld_out % 8 == 0;
+  e = dy_dt == HSTU_BF16   ? sum_rows<HSTU_BF16>(a, L.runs, vec, s)
+      : dy_dt == HSTU_FP16 ? sum_rows<HSTU_FP16>(a, L.runs, vec, s)
+                           : sum_rows<HSTU_FP32>(a, L.runs, vec, s);
+  return cuda_status(e, "embed_bwd: sums");
+}
+
+template <int DT>
+cudaError_t lookup(const LookupArgs& a, bool vec, int threads, int grid, cudaStream_t s) {
+  LaunchScope ls(K_EMBED_LOOKUP, s);
+  if (vec)
+    k_embed_lookup<DT, true><<<grid, threads, 0, s>>>(a);
+  else
+    k_embed_lookup<DT, false><<<grid, threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace hstu
+
+// ---------------------------------------------------------------- C ABI
+extern "C" {
+
+size_t hstu_embed_workspace_size(void) { return 256; }
+
+hstu_status hstu_embed_fwd(int64_t n_tokens, const int64_t* ids, const void* table,
+                           int32_t table_dtype, int64_t n_rows, int32_t d, int64_t ld_table,
+                           int64_t pad_id, float scale, void* out, int32_t out_dtype,
+                           int64_t ld_out, void* ws, size_t ws_bytes, void* stream) {
+  using namespace hstu;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n_tokens < 0 || n_tokens > kMaxTokens || n_rows < 1 || n_rows > kMaxRows || d < 1 ||
+      d > (1 << 20) || ld_table < d || ld_out < d || !dtype_ok(table_dtype) || !dtype_ok(out_dtype))
+    return HSTU_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return HSTU_ERR_INVALID_ARG;  // NaN or infinite
+  if (n_tokens > 0 && (!ids || !table || !out)) return HSTU_ERR_INVALID_ARG;
+  if (!al16(ids) || !al16(table) || !al16(out)) return HSTU_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < hstu_embed_workspace_size() || !al256(ws)) return HSTU_ERR_WORKSPACE;
+  LookupArgs a{};
+  a.ids = ids;
+  a.table = table;
+  a.out = out;
+  a.status = static_cast<int*>(ws);
+  a.T = n_tokens;
+  a.R = n_rows;
+  a.ldt = ld_table;
+  a.ldo = ld_out;
+  a.pad = pad_id;
+  a.scale = scale;
+  a.out_dt = out_dtype;
+  a.d = d;
+  a.check = n_tokens <= kCheckMax;
+  const bool vec = d % 8 == 0 && ld_table % 8 == 0 && ld_out % 8 == 0;
+  const int n_cols = vec ? d / 8 : d;
+  a.cols = n_cols <= 256 ? n_cols : 256;
+  const int rows = std::max(1, 256 / a.cols);
+  const int threads = a.cols * rows;
+  const int64_t per = (int64_t)rows * kLookupUnroll;
+  const int64_t blocks = std::min<int64_t>((n_tokens + per - 1) / per, (int64_t)num_sms() * 16);
+  if (!a.check) {
+    const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), s);
+    if (e != cudaSuccess) return cuda_status(e, "hstu_embed_fwd");
+  }
+  const int grid = (int)blocks + a.check;
+  const cudaError_t e = table_dtype == HSTU_BF16   ? lookup<HSTU_BF16>(a, vec, threads, grid, s)
+                        : table_dtype == HSTU_FP16 ? lookup<HSTU_FP16>(a, vec, threads, grid, s)
+                                                   : lookup<HSTU_FP32>(a, vec, threads, grid, s);
+  return cuda_status(e, "hstu_embed_fwd");
+}
+
+size_t hstu_embed_bwd_workspace_size(int64_t n_tokens, int64_t n_rows, int32_t d) {
+  hstu::BwdLayout L;
+  return hstu::bwd_layout(n_tokens, n_rows, d, &L) ? L.total : 0;
+}
+
+hstu_status hstu_embed_bwd(int64_t n_tokens, const int64_t* ids, const void* dY, int32_t dy_dtype,
+                           int64_t ld_dy, int64_t n_rows, int32_t d, int64_t pad_id, float scale,
+                           int32_t accumulate, void* dE, int32_t de_dtype, int64_t ld_de, void* ws,
+                           size_t ws_bytes, void* stream) {
+  return hstu::embed_bwd(n_tokens, ids, dY, dy_dtype, ld_dy, n_rows, d, pad_id, scale, accumulate,
+                         0, nullptr, nullptr, dE, de_dtype, ld_de, ws, ws_bytes,
+                         static_cast<cudaStream_t>(stream));
+}
+
+hstu_status hstu_embed_bwd_rows(int64_t n_tokens, const int64_t* ids, const void* dY,
+                                int32_t dy_dtype, int64_t ld_dy, int64_t n_rows, int32_t d,
+                                int64_t pad_id, float scale, int64_t* row_ids, void* rows,
+                                int32_t rows_dtype, int64_t ld_rows, int64_t* n_unique, void* ws,
+                                size_t ws_bytes, void* stream) {
+  return hstu::embed_bwd(n_tokens, ids, dY, dy_dtype, ld_dy, n_rows, d, pad_id, scale, 0, 1,
+                         row_ids, n_unique, rows, rows_dtype, ld_rows, ws, ws_bytes,
+                         static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

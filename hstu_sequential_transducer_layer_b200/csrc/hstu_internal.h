@@ -54,7 +54,13 @@ enum KernelId : int32_t {
   K_SUM_ROWS = 35,
   K_F32_TO_F16 = 36,
   K_LN_COEF = 37,
-  K_NUM_KERNELS = 38
+  K_EMBED_LOOKUP = 38,
+  K_EMBED_SORT = 39,
+  K_EMBED_SUM = 40,
+  K_EMBED_JOIN = 41,
+  K_GRAD_NORM = 42,
+  K_ADAMW = 43,
+  K_NUM_KERNELS = 44
 };
 const char* kernel_name(int id);
 

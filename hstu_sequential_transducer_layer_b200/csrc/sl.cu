@@ -45,12 +45,6 @@ __host__ __device__ __forceinline__ int64_t sl_keep(int64_t n) {
   return k < 1 ? 1 : k;
 }
 
-// Programmatic dependent launch: a kernel launched with programmatic stream
-// serialization may start while its predecessor runs; griddepcontrol.wait
-// returns once the predecessor grid has finished and its writes are visible.
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
-
 __global__ void __launch_bounds__(1024)
     k_sl_offsets(const int64_t* __restrict__ raw_off, int64_t B, int64_t raw_total,
                  int64_t max_raw_len, int64_t* __restrict__ out_off, int* status) {
@@ -90,31 +84,6 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == blockDim.x - 1) s_carry += s_part[threadIdx.x];
     __syncthreads();
   }
-}
-
-// Block-wide exclusive scan of one int per thread (NT threads): returns this
-// thread's prefix; *total receives the block's sum.  Used on packed pairs of
-// 16-bit counts too (no field overflows: a block counts at most 4096).
-template <int NT>
-__device__ __forceinline__ int block_excl_scan(int v, int* s_warp, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  __syncthreads();  // s_warp is free (previous use done)
-  if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    before += w < warp ? s_warp[w] : 0;
-    all += s_warp[w];
-  }
-  *total = all;
-  return before + incl - v;
 }
 
 // Selection block size, positions per thread in one compaction chunk, the
@@ -297,7 +266,9 @@ __global__ void __launch_bounds__(kSelThreads)
 // timestamp are read, the timestamp replaces the code, and the embedding row
 // is copied (16 bytes per lane).  A warp takes 8 rows at a time: lanes 0..7
 // read the codes, ids and timestamps; the warp then copies two rows at a
-// time, 8 loads in flight per lane.
+// time, 8 loads in flight per lane.  out_ids (optional) receives each kept
+// token's row in the two tables taken as one, the action rows behind the
+// content rows.
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 8;
 constexpr int kCopyWords = 4;
@@ -306,7 +277,8 @@ __global__ void __launch_bounds__(kGatherThreads, 4)
     k_sl_gather(const int64_t* __restrict__ total, const int64_t* __restrict__ ids,
                 const int64_t* __restrict__ ts, const __nv_bfloat16* __restrict__ ctab,
                 int64_t n_content, const __nv_bfloat16* __restrict__ atab, int64_t n_action,
-                int d, __nv_bfloat16* __restrict__ X, int64_t* __restrict__ out_ts, int* status) {
+                int d, __nv_bfloat16* __restrict__ X, int64_t* __restrict__ out_ts,
+                int64_t* __restrict__ out_ids, int* status) {
   // No early exit on the status word: a bad id found by one block must not
   // stop the others (bad offsets leave *total = 0, so nothing runs then).
   grid_dep_wait();  // k_sl_select has written every code
@@ -332,6 +304,7 @@ __global__ void __launch_bounds__(kGatherThreads, 4)
       else
         atomicCAS(status, HSTU_OK, HSTU_ERR_BAD_IDS);
       out_ts[t0 + lane] = tsv;
+      if (out_ids) out_ids[t0 + lane] = src ? id + (action ? n_content : 0) : -1;
     }
     uint4* dst = reinterpret_cast<uint4*>(X + t0 * (int64_t)d);
     for (int r = 0; r < nb; r += 2) {
@@ -374,12 +347,13 @@ int64_t hstu_sl_keep_count(int64_t n) {
   return (n < 0 || n > hstu::kSlMaxLen) ? -1 : hstu::sl_keep(n);
 }
 
-hstu_status hstu_sl_embed(int64_t B, int64_t raw_total, int64_t max_raw_len,
-                          const int64_t* raw_offsets, const int64_t* raw_ids,
-                          const int64_t* raw_timestamps, uint64_t seed, const void* content_table,
-                          int64_t n_content, const void* action_table, int64_t n_action,
-                          int32_t d_model, int64_t* out_offsets, void* out_X,
-                          int64_t* out_timestamps, void* ws, size_t ws_bytes, void* stream_ptr) {
+static hstu_status sl_embed(int64_t B, int64_t raw_total, int64_t max_raw_len,
+                            const int64_t* raw_offsets, const int64_t* raw_ids,
+                            const int64_t* raw_timestamps, uint64_t seed,
+                            const void* content_table, int64_t n_content, const void* action_table,
+                            int64_t n_action, int32_t d_model, int64_t* out_offsets, void* out_X,
+                            int64_t* out_timestamps, int64_t* out_ids, void* ws, size_t ws_bytes,
+                            void* stream_ptr) {
   using namespace hstu;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (B < 0 || raw_total < 0 || max_raw_len < 0 || d_model <= 0 || d_model % 8 != 0)
@@ -441,11 +415,36 @@ hstu_status hstu_sl_embed(int64_t B, int64_t raw_total, int64_t max_raw_len,
                              static_cast<const __nv_bfloat16*>(content_table), n_content,
                              static_cast<const __nv_bfloat16*>(action_table), n_action,
                              (int)d_model, static_cast<__nv_bfloat16*>(out_X), out_timestamps,
-                             status) != cudaSuccess)
+                             out_ids, status) != cudaSuccess)
         return HSTU_ERR_CUDA;
     }
   }
   return HSTU_OK;
+}
+
+hstu_status hstu_sl_embed(int64_t B, int64_t raw_total, int64_t max_raw_len,
+                          const int64_t* raw_offsets, const int64_t* raw_ids,
+                          const int64_t* raw_timestamps, uint64_t seed, const void* content_table,
+                          int64_t n_content, const void* action_table, int64_t n_action,
+                          int32_t d_model, int64_t* out_offsets, void* out_X,
+                          int64_t* out_timestamps, void* ws, size_t ws_bytes, void* stream) {
+  return sl_embed(B, raw_total, max_raw_len, raw_offsets, raw_ids, raw_timestamps, seed,
+                  content_table, n_content, action_table, n_action, d_model, out_offsets, out_X,
+                  out_timestamps, nullptr, ws, ws_bytes, stream);
+}
+
+hstu_status hstu_sl_embed_ids(int64_t B, int64_t raw_total, int64_t max_raw_len,
+                              const int64_t* raw_offsets, const int64_t* raw_ids,
+                              const int64_t* raw_timestamps, uint64_t seed,
+                              const void* content_table, int64_t n_content,
+                              const void* action_table, int64_t n_action, int32_t d_model,
+                              int64_t* out_offsets, void* out_X, int64_t* out_timestamps,
+                              int64_t* out_ids, void* ws, size_t ws_bytes, void* stream) {
+  if ((raw_total > 0 && !out_ids) || (reinterpret_cast<uintptr_t>(out_ids) & 15))
+    return HSTU_ERR_INVALID_ARG;
+  return sl_embed(B, raw_total, max_raw_len, raw_offsets, raw_ids, raw_timestamps, seed,
+                  content_table, n_content, action_table, n_action, d_model, out_offsets, out_X,
+                  out_timestamps, out_ids, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -92,10 +92,12 @@ typedef enum {
   HSTU_ERR_BAD_OFFSETS = 5,   /* device: offsets not monotone, wrong total, length > max */
   HSTU_ERR_TIMEOUT = 6,       /* device: an in-kernel wait gave up */
   HSTU_ERR_BAD_TIMESTAMPS = 7, /* device: a user's timestamps span 2^30 s or more */
-  HSTU_ERR_BAD_IDS = 8         /* device: a token id outside its embedding table */
+  HSTU_ERR_BAD_IDS = 8         /* device: a token or row id outside its embedding table */
 } hstu_status;
 
-typedef enum { HSTU_BF16 = 0, HSTU_FP32 = 1 } hstu_dtype;
+/* Layers are HSTU_BF16 or HSTU_FP32; the embedding and optimizer entry points
+ * take all three. */
+typedef enum { HSTU_BF16 = 0, HSTU_FP32 = 1, HSTU_FP16 = 2 } hstu_dtype;
 
 /* Shape of one layer (all layers of a stack share it). */
 typedef struct {
@@ -375,6 +377,155 @@ hstu_status hstu_sl_embed(int64_t B, int64_t raw_total, int64_t max_raw_len,
                           const void* action_table, int64_t n_action, int32_t d_model,
                           int64_t* out_offsets, void* out_X, int64_t* out_timestamps,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* hstu_sl_embed that also writes, for every kept token, the row it was copied
+ * from: out_ids (device int64 [sum k_b], 16-byte aligned) holds a content
+ * item's row of content_table, and n_content + the row of action_table for an
+ * action, i.e. rows of the two tables taken as one table with the actions
+ * behind the content (-1 for an id outside its table).  Those are the ids
+ * that hstu_embed_bwd takes for the gradient of such a table. */
+hstu_status hstu_sl_embed_ids(int64_t B, int64_t raw_total, int64_t max_raw_len,
+                              const int64_t* raw_offsets, const int64_t* raw_ids,
+                              const int64_t* raw_timestamps, uint64_t seed,
+                              const void* content_table, int64_t n_content,
+                              const void* action_table, int64_t n_action, int32_t d_model,
+                              int64_t* out_offsets, void* out_X, int64_t* out_timestamps,
+                              int64_t* out_ids, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Embedding lookup with scaling: out[t, :] = scale * table[ids[t], :], the
+ * product in fp32 and rounded once to out_dtype.
+ *   ids     device int64 [n_tokens]; a token whose id is pad_id gets a zero
+ *           row (pass -1 for no padding; any id may be the padding's)
+ *   table   device [n_rows, d] of table_dtype, ld_table elements apart
+ *   out     device [n_tokens, d] of out_dtype, ld_out elements apart; the gap
+ *           behind each row is left as it was
+ * Any d up to 2^20 and any strides; rows are moved 16 bytes at a time where d
+ * and both strides are multiples of 8, else element by element.  n_tokens and
+ * n_rows below 2^31 - 8192.  An id outside the table that is not pad_id gets a
+ * zero row and sets HSTU_ERR_BAD_IDS in the workspace's status word
+ * (hstu_embed_workspace_size() bytes, 256-byte aligned).  Asynchronous on
+ * `stream`. */
+size_t hstu_embed_workspace_size(void);
+hstu_status hstu_embed_fwd(int64_t n_tokens, const int64_t* ids, const void* table,
+                           int32_t table_dtype, int64_t n_rows, int32_t d, int64_t ld_table,
+                           int64_t pad_id, float scale, void* out, int32_t out_dtype,
+                           int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the lookup: row r of the table's gradient is scale * the sum of
+ * dY[t, :] over the tokens with ids[t] = r, summed in fp32 and rounded once.
+ * The tokens are sorted by (id, t) first, so every sum has one order and the
+ * result is the same bit for bit on every run.  Tokens of pad_id and of ids
+ * outside the table take no part (the latter set HSTU_ERR_BAD_IDS).
+ * hstu_embed_bwd writes the whole gradient dE [n_rows, d] (rows without
+ * tokens become zero), or with accumulate = 1 adds into it (rows without
+ * tokens are not touched).  hstu_embed_bwd_rows writes the touched rows only:
+ *   n_unique  device int64 [1]: their number U
+ *   row_ids   device int64 [min(n_tokens, n_rows)]: the first U entries are
+ *             the touched rows, ascending
+ *   rows      device [min(n_tokens, n_rows), d] of rows_dtype, ld_rows
+ *             elements apart: the first U rows are their gradients
+ * What lies behind the first U entries and rows is left as it was.  This is
+ * the form that hstu_adamw_step and hstu_grad_norm take.  Workspace:
+ * hstu_embed_bwd_workspace_size() bytes (0 if the arguments are invalid),
+ * 256-byte aligned; limits and strides as for hstu_embed_fwd. */
+size_t hstu_embed_bwd_workspace_size(int64_t n_tokens, int64_t n_rows, int32_t d);
+hstu_status hstu_embed_bwd(int64_t n_tokens, const int64_t* ids, const void* dY, int32_t dy_dtype,
+                           int64_t ld_dy, int64_t n_rows, int32_t d, int64_t pad_id, float scale,
+                           int32_t accumulate, void* dE, int32_t de_dtype, int64_t ld_de,
+                           void* workspace, size_t workspace_bytes, void* stream);
+hstu_status hstu_embed_bwd_rows(int64_t n_tokens, const int64_t* ids, const void* dY,
+                                int32_t dy_dtype, int64_t ld_dy, int64_t n_rows, int32_t d,
+                                int64_t pad_id, float scale, int64_t* row_ids, void* rows,
+                                int32_t rows_dtype, int64_t ld_rows, int64_t* n_unique,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* One tensor of an optimizer step (all pointers but the struct itself are
+ * device pointers, 16-byte aligned except where noted).  Dense: row_ids and
+ * n_rows null; `grad`, `param` and the states hold n elements.  Row-sparse (an
+ * embedding table with the gradient of hstu_embed_bwd_rows): the parameter and
+ * its states are [n / row_len, row_len], contiguous; `grad` holds up to
+ * max_rows rows, of which the first *n_rows belong to the table rows
+ * row_ids[0 .. *n_rows), strictly ascending.  Rows without a gradient, their
+ * states and the weight decay on them are not touched. */
+#define HSTU_STATE_BLOCK 256  /* elements that share a scale in 8-bit states */
+#define HSTU_MAX_TENSORS 4096
+typedef struct {
+  int64_t n;               /* elements of the parameter */
+  int64_t row_len;         /* row-sparse only: elements of a row */
+  int64_t max_rows;        /* row-sparse only: rows allocated in grad and row_ids */
+  const int64_t* row_ids;  /* row-sparse only */
+  const int64_t* n_rows;   /* row-sparse only: number of rows in use (8-byte aligned) */
+  const void* grad;        /* of grad_dtype */
+  void* param;             /* of param_dtype, updated */
+  float* master;           /* optional fp32 copy of a 16-bit param: read and updated in its
+                            * place; param then receives the rounded result */
+  void* copy_f16;          /* optional: receives the new (rounded) param as fp16, saturating at
+                            * +-65504, as hstu_bf16_to_f16 does (W1_f16, W2_f16) */
+  void* m;                 /* first moment: fp32, or e4m3 codes */
+  void* v;                 /* second moment: fp32; 8-bit: e4m3 codes of its square root */
+  uint8_t* m_scale;        /* 8-bit states: one byte per block of 256 elements (any alignment) */
+  uint8_t* v_scale;
+  double weight_decay;
+  int32_t grad_dtype;      /* hstu_dtype */
+  int32_t param_dtype;     /* hstu_dtype */
+  int32_t state_bits;      /* 32 or 8 */
+} hstu_adamw_tensor;
+
+/* Global gradient norm over a list of tensors, one reading of every gradient:
+ * out[0] = sqrt(sum of all squares) (squares and sums in fp64) and out[1] =
+ * the factor that clips it, min(1, max_norm / norm), or NaN when the norm is
+ * not finite; out: device fp32 [2], 16-byte aligned.  Only the gradient's
+ * fields of each tensor are read (n, grad, grad_dtype, and for a row-sparse
+ * one row_len, max_rows, n_rows).  max_norm > 0 (infinity: never clips).  At
+ * most HSTU_MAX_TENSORS tensors (host array).  Deterministic on one device. */
+size_t hstu_grad_norm_workspace_size(void);
+hstu_status hstu_grad_norm(const hstu_adamw_tensor* tensors, int32_t n_tensors, double max_norm,
+                           float* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One AdamW step (decoupled weight decay) of a list of tensors.  With
+ * g = grad_scale * grad and t = step, per element
+ *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32 (the constants from doubles); p is the master where there is one.
+ * 8-bit states: m and r = sqrt(v) are held as e4m3 codes (4 exponent and 3
+ * significand bits) times a power of two per block of 256 consecutive
+ * elements (of one row, in a row-sparse tensor, which then has
+ * ceil(row_len / 256) blocks per row): scale byte s stands for 2^(s - 127),
+ * chosen so that the block's largest finite magnitude lies in [2^7, 2^8).
+ * The update uses the unrounded moments; what is stored is rounded up or down
+ * to a neighbouring code at random, with the probability that makes the mean
+ * (of m and of r) right, because v moves by 1 - beta2 of itself per step, far
+ * less than half a code, and would stand still under rounding to nearest.  The random number
+ * is a function of (seed, step, position of the tensor in the list, element)
+ * alone.  Moments that are not finite are stored as NaN.  Buffers of zeros are
+ * valid initial states in either form.
+ *   grad_scale  optional device fp32: e.g. out[1] of hstu_grad_norm.  If it is
+ *               not finite the step changes nothing.
+ *   step_dev    optional device int64, read instead of `step` (for a step
+ *               captured into a graph; advance it between replays); a value
+ *               below 1 sets HSTU_ERR_INVALID_ARG and changes nothing
+ *   lr_dev      optional device fp32, read instead of `lr`
+ * Row ids out of range or not ascending, and a row count above max_rows or
+ * below 0, set HSTU_ERR_BAD_IDS; such rows are skipped (rows given twice
+ * without being adjacent have an unspecified result).  No two tensors may
+ * share memory.  Workspace: hstu_adamw_workspace_size() bytes, 256-byte
+ * aligned (the status word).  Asynchronous on `stream`. */
+typedef struct {
+  double lr;
+  double beta1;            /* [0, 1) */
+  double beta2;            /* [0, 1) */
+  double eps;              /* > 0 */
+  int64_t step;            /* >= 1 */
+  const int64_t* step_dev;
+  const float* lr_dev;
+  const float* grad_scale;
+  uint64_t seed;           /* of the 8-bit states' rounding */
+} hstu_adamw_args;
+size_t hstu_adamw_workspace_size(void);
+hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor* tensors,
+                            int32_t n_tensors, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 /* Synchronises `stream`, then returns the device status word that the last
  * call using this workspace left (HSTU_OK if none of its checks failed). */

@@ -1,0 +1,435 @@
+"""GPU parity of the global gradient norm and of the AdamW step against
+float64 (oracle.training).
+
+Bounds, with e = 2^-24 (half a step of fp32): m is two products and a sum of
+constants that are themselves rounded, at most 4e (|beta1 m| + |(1 - beta1) g|);
+v likewise at most 6e of itself; the update u = lr m / (1 - beta1^t) / (sqrt(v /
+(1 - beta2^t)) + eps) adds at most 16e |u| (a quotient to 2 ulp, a root, five
+products and sums, and half of v's error) to what m's error makes of it; p adds
+3e (|p| + |u|).  A 16-bit parameter is off by half a step of its type more:
+that is relative to the value for normal numbers, and 2^-25 for fp16 values
+below 2^-14, whose step is 2^-24 throughout."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import training as TR
+
+pytestmark = pytest.mark.gpu
+
+BAD_IDS, INVALID = 8, 1
+E = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 0.0}
+TINY = {"bf16": 0.0, "f16": 2.0 ** -25, "f32": 0.0}
+HYPER = dict(lr=1e-2, beta1=0.9, beta2=0.99, eps=1e-8)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from hstu_sequential_transducer_layer_b200.build import build
+    build()
+
+
+def _dt(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[name]
+
+
+def _ws(n):
+    import torch
+    return torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+
+
+def _np(x):
+    return x.detach().double().cpu().numpy()
+
+
+# ---------------------------------------------------------------- norm
+@pytest.mark.parametrize("sizes", [[], [0], [1], [3, 0, 5], [4096], [4097, 8191, 7],
+                                   [300000, 1, 77777], [5] * 300, [3] * 600])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_norm(sizes, dtype):
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    g = [torch.randn(n, device="cuda").to(_dt(dtype)) for n in sizes]
+    lst = H.GradTensors([dict(grad=x) for x in g])
+    out, ws = torch.full((2,), -1.0, device="cuda"), _ws(H.hstu_grad_norm_workspace_size())
+    for max_norm in (0.5, 1e9):
+        H.hstu_grad_norm(lst, max_norm, out, ws)
+        n, c = TR.grad_norm([_np(x) for x in g], max_norm)
+        got = out.tolist()
+        # fp64 sums: only the rounding to fp32 shows
+        assert abs(got[0] - n) <= 1.01 * E * n and abs(got[1] - c) <= 1.01 * E * c
+        assert H.hstu_read_status(ws) == 0
+
+
+def test_norm_extremes_and_rows():
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    out, ws = torch.zeros(2, device="cuda"), _ws(H.hstu_grad_norm_workspace_size())
+    big = torch.tensor([3e30, 4e30], device="cuda")
+    small = torch.tensor([3e-30, 4e-30], device="cuda")
+    for x, n in ((big, 5e30), (small, 5e-30)):           # squares beyond fp32's range
+        H.hstu_grad_norm(H.GradTensors([dict(grad=x)]), 1.0, out, ws)
+        assert abs(float(out[0]) / n - 1) < 1e-6
+        assert abs(float(out[1]) - min(1.0, 1 / n)) <= 1e-6 * min(1.0, 1 / n)
+    H.hstu_grad_norm(H.GradTensors([dict(grad=torch.zeros(9, device="cuda"))]), 1.0, out, ws)
+    assert out.tolist() == [0.0, 1.0]
+    H.hstu_grad_norm(H.GradTensors([dict(grad=big)]), math.inf, out, ws)
+    assert float(out[1]) == 1.0
+    for x in (math.nan, math.inf, -math.inf):
+        bad = torch.ones(10000, device="cuda")
+        bad[7777] = x
+        H.hstu_grad_norm(H.GradTensors([dict(grad=bad), dict(grad=big)]), 1.0, out, ws)
+        assert math.isnan(float(out[1])) and not math.isfinite(float(out[0]))
+    # only the first n_rows rows count; a count outside [0, rows] is cut
+    rows = torch.randn(100, 33, device="cuda")
+    rows[60:] = math.nan
+    n = torch.zeros(1, dtype=torch.int64, device="cuda")
+    lst = H.GradTensors([dict(grad=rows, n_rows=n), dict(grad=big[:1] * 0 + 2)])
+    for k in (0, 1, 59, 60, -4):
+        n.fill_(k)
+        H.hstu_grad_norm(lst, 1.0, out, ws)
+        want = TR.grad_norm([_np(rows[:max(k, 0)]), np.array([2.0])], 1.0)
+        assert abs(float(out[0]) - want[0]) <= 1.01 * E * want[0]
+    n.fill_(1 << 60)
+    H.hstu_grad_norm(lst, 1.0, out, ws)
+    assert math.isnan(float(out[0]))                      # all 100 rows, the NaN ones among them
+
+
+# ---------------------------------------------------------------- AdamW
+def _bounds(p, g, m, v, step, wd, gs, h=HYPER):
+    """(p, m, v) in float64 and how far fp32 may be from each."""
+    rp, rm, rv = TR.adamw(p, g, m, v, step, h["lr"], h["beta1"], h["beta2"], h["eps"], wd, gs)
+    dm = 4 * E * (np.abs(h["beta1"] * m) + np.abs((1 - h["beta1"]) * g * gs))
+    den = np.sqrt(rv / (1 - h["beta2"] ** step)) + h["eps"]
+    unit = h["lr"] / (1 - h["beta1"] ** step) / den
+    u = unit * np.abs(rm)
+    dp = unit * dm + 16 * E * u + 3 * E * (np.abs(p) + u)
+    return rp, rm, rv, dp, dm, 6 * E * rv
+
+
+def _make(n, param, grad, master, bits, seed, shape=None, zero=False):
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda s: torch.randn(*(shape or (n,)), device="cuda", generator=g) * s  # noqa: E731
+    p = r(1.0)
+    t = dict(param=p.to(_dt(param)), grad=r(0.1).to(_dt(grad)))
+    if master:
+        t["master"] = p.clone()
+    if bits == 32:
+        t["m"], t["v"] = r(0.02) * (not zero), (r(0.02) * (not zero)).square()
+    else:
+        s = shape or (n,)
+        k = H.state_scales(s)
+        code = lambda top: torch.randint(0, top, s, device="cuda", generator=g)  # noqa: E731
+        sign = code(2) * 128
+        t["m"] = ((code(0x7E) + sign) * (not zero)).to(torch.uint8)
+        t["v"] = (code(0x7E) * (not zero)).to(torch.uint8)
+        for q, e in (("m_scale", 118), ("v_scale", 117)):
+            t[q] = (torch.randint(e - 2, e + 3, (k,), device="cuda", generator=g)
+                    * (not zero)).to(torch.uint8)
+    return t
+
+
+def _copy(t):
+    return {k: (x.clone() if hasattr(x, "clone") else x) for k, x in t.items()}
+
+
+def _blocks(x, rows=None):
+    """Array [blocks, 256] of a tensor (of each row of it), zeros behind the end."""
+    x = x.reshape(1, -1) if rows is None else x.reshape(rows, -1)
+    n = -(-x.shape[1] // 256) * 256
+    return np.pad(x, ((0, 0), (0, n - x.shape[1]))).reshape(-1, 256)
+
+
+def _check(old, new, step, gs, ordinal, seed, hyper=HYPER, name="bf16"):
+    """One dense tensor: new against the oracle's step of old."""
+    import torch
+    wd = old.get("weight_decay", 0.0)
+    p = _np(old["master"] if "master" in old else old["param"])
+    g = _np(old["grad"])
+    if old["m"].dtype == torch.float32:
+        m, v = _np(old["m"]), _np(old["v"])
+    else:
+        co = {k: old[k].view(torch.uint8).cpu().numpy() for k in ("m", "v", "m_scale", "v_scale")}
+        m = TR.decode(_blocks(co["m"]), co["m_scale"]).ravel()[:p.size]
+        v = TR.decode(_blocks(co["v"]), co["v_scale"]).ravel()[:p.size] ** 2
+    rp, rm, rv, dp, dm, dv = _bounds(p, g, m, v, step, wd, gs, hyper)
+    if "master" in new:
+        assert (np.abs(_np(new["master"]) - rp) <= dp).all()
+    assert (np.abs(_np(new["param"]) - rp) <= dp * 1.01 + HALF[name] * np.abs(rp) + TINY[name]).all()
+    if "copy_f16" in new:
+        want = new["param"].float().clamp(-65504, 65504).half()
+        assert torch.equal(new["copy_f16"], want)
+    if old["m"].dtype == torch.float32:
+        assert (np.abs(_np(new["m"]) - rm) <= dm).all() and (np.abs(_np(new["v"]) - rv) <= dv).all()
+        return
+    nb = -(-p.size // 256)
+    cm, sm, cr, sr = TR.adamw_step_8bit(
+        _blocks(co["m"]), co["m_scale"], _blocks(co["v"]), co["v_scale"], _blocks(g).astype(np.float32),
+        seed, step, ordinal, np.arange(nb), hyper["beta1"], hyper["beta2"], np.float32(gs))
+    for k, want in (("m", cm), ("v", cr)):
+        np.testing.assert_array_equal(new[k].view(torch.uint8).cpu().numpy(), want.ravel()[:p.size])
+    np.testing.assert_array_equal(new["m_scale"].cpu().numpy(), sm)
+    np.testing.assert_array_equal(new["v_scale"].cpu().numpy(), sr)
+
+
+SIZES = [1, 3, 255, 256, 257, 2047, 2048, 2051, 70001]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("param,grad,master", [("bf16", "f32", True), ("bf16", "bf16", False),
+                                               ("f32", "f32", False), ("f16", "f16", True),
+                                               ("f32", "bf16", False), ("f16", "f32", False)])
+def test_adamw_step(bits, param, grad, master):
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    ts = []
+    for i, n in enumerate(SIZES):
+        t = _make(n, param, grad, master, bits, seed=i)
+        t["weight_decay"] = 0.1 * (i % 2)
+        if i % 3 != 1:
+            t["copy_f16"] = torch.zeros(n, dtype=torch.float16, device="cuda")
+        ts.append(t)
+    old = [_copy(t) for t in ts]
+    lst, ws = H.AdamWTensors(ts), _ws(256)
+    gs = torch.tensor([0.37], device="cuda")
+    for step in (1, 12345):
+        H.hstu_adamw_step(lst, ws, step=step, grad_scale=gs, seed=99, **HYPER)
+        assert H.hstu_read_status(ws) == 0
+        for i, t in enumerate(ts):
+            _check(old[i], t, step, float(gs), i, 99, name=param)
+        old = [_copy(t) for t in ts]
+
+
+def test_adamw_first_step_from_zeros_and_large_values():
+    """Zero states; then gradients and parameters over many magnitudes (a
+    parameter beyond fp16's range saturates its fp16 copy)."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    for bits in (32, 8):
+        t = _make(3000, "bf16", "f32", True, bits, 3, zero=True)
+        t["grad"] *= torch.exp(torch.linspace(-18, 18, 3000, device="cuda"))
+        t["grad"][:256] = 0
+        t["master"][5], t["param"][5] = 1e6, 1e6
+        t["copy_f16"] = torch.zeros(3000, dtype=torch.float16, device="cuda")
+        old = _copy(t)
+        H.hstu_adamw_step(H.AdamWTensors([t]), _ws(256), step=1, **HYPER)
+        _check(old, t, 1, 1.0, 0, 0)
+        assert float(t["copy_f16"][5]) == 65504.0
+
+
+def test_many_tensors():
+    """More tensors than one launch takes, empty ones among them."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    ts = [_make(1 + 37 * (i % 9), "bf16", "f32", True, 8 if i % 2 else 32, i) for i in range(600)]
+    for i in (0, 100, 300, 599):
+        ts[i] = {k: x[:0].contiguous() for k, x in ts[i].items()}
+    old = [_copy(t) for t in ts]
+    lst, ws = H.AdamWTensors(ts), _ws(256)
+    H.hstu_adamw_step(lst, ws, step=7, seed=5, **HYPER)
+    for i, t in enumerate(ts):
+        if t["param"].numel():
+            _check(old[i], t, 7, 1.0, i, 5)
+    H.hstu_adamw_step(H.AdamWTensors([]), ws, step=1, lr=1e-3)
+    assert H.hstu_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("R,d,U,cap", [(1, 1, 1, 1), (9, 50, 0, 4), (9, 50, 9, 9), (300, 257, 77, 90),
+                                       (300, 256, 77, 300), (1000, 8, 400, 401), (64, 1024, 33, 50)])
+def test_touched_rows(R, d, U, cap, bits):
+    """Rows of a table: those of the list as the dense step would, every other
+    row's parameter and state as before."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    t = _make(0, "bf16", "f32", True, bits, R + d, shape=(R, d))
+    rng = np.random.default_rng(R)
+    rows = np.sort(rng.permutation(R)[:U])
+    t["grad"] = torch.full((cap, d), math.nan, device="cuda")
+    t["grad"][:U] = torch.randn(U, d, device="cuda") * 0.1
+    t["row_ids"] = torch.full((cap,), -1, dtype=torch.int64, device="cuda")
+    t["row_ids"][:U] = torch.from_numpy(rows).cuda()
+    t["n_rows"] = torch.tensor([U], device="cuda")
+    t["weight_decay"], t["copy_f16"] = 0.1, torch.zeros(R, d, dtype=torch.float16, device="cuda")
+    old = _copy(t)
+    ws = _ws(256)
+    dense = _make(100, "f32", "f32", False, bits, 1)      # the table is the list's second tensor
+    H.hstu_adamw_step(H.AdamWTensors([dense, t]), ws, step=4, seed=11, **HYPER)
+    assert H.hstu_read_status(ws) == 0
+    rest = np.setdiff1d(np.arange(R), rows)
+    nb = -(-d // 256)
+    for k in ("param", "master", "m", "v", "copy_f16"):
+        assert torch.equal(t[k].view(R, d)[rest], old[k].view(R, d)[rest])
+    if U == 0:
+        return
+    g = _np(t["grad"][:U])
+    p = _np(old["master"])[rows]
+    if bits == 32:
+        m, v = _np(old["m"])[rows], _np(old["v"])[rows]
+    else:
+        cod = {k: old[k].cpu().numpy() for k in ("m", "v", "m_scale", "v_scale")}
+        at = (rows[:, None] * nb + np.arange(nb)).ravel()
+        wide = {k: _blocks(cod[k][rows], U) for k in ("m", "v")}
+        dec = lambda k: TR.decode(wide[k], cod[k + "_scale"][at]).reshape(U, -1)[:, :d]  # noqa: E731
+        m, v = dec("m"), dec("v") ** 2
+    rp, rm, rv, dp, dm, dv = _bounds(p, g, m, v, 4, 0.1, 1.0)
+    assert (np.abs(_np(t["master"])[rows] - rp) <= dp).all()
+    assert (np.abs(_np(t["param"])[rows] - rp) <= dp * 1.01 + 2.0 ** -8 * np.abs(rp)).all()
+    if bits == 32:
+        assert (np.abs(_np(t["m"])[rows] - rm) <= dm).all()
+        assert (np.abs(_np(t["v"])[rows] - rv) <= dv).all()
+        return
+    cm, sm, cr, sr = TR.adamw_step_8bit(wide["m"], cod["m_scale"][at], wide["v"], cod["v_scale"][at],
+                                        _blocks(g, U).astype(np.float32), 11, 4, 1, at,
+                                        HYPER["beta1"], HYPER["beta2"])
+    cut = lambda c: c.reshape(U, -1)[:, :d]  # noqa: E731
+    np.testing.assert_array_equal(t["m"].cpu().numpy()[rows], cut(cm))
+    np.testing.assert_array_equal(t["v"].cpu().numpy()[rows], cut(cr))
+    np.testing.assert_array_equal(t["m_scale"].cpu().numpy()[at], sm)
+    np.testing.assert_array_equal(t["v_scale"].cpu().numpy()[at], sr)
+    others = np.setdiff1d(np.arange(R * nb), at)
+    assert torch.equal(t["m_scale"][others], old["m_scale"][others])
+
+
+def test_bad_rows_are_skipped_and_reported():
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    for ids, n, good in (([1, 5, 20], 3, [1, 5]), ([-1, 3, 4], 3, [3, 4]), ([2, 2, 6], 3, [2, 6]),
+                         ([7, 3, 8], 3, [7, 8]), ([1, 2, 3], 4, [1, 2, 3]), ([1, 2, 3], -1, [])):
+        t = _make(0, "f32", "f32", False, 32, 1, shape=(10, 16))
+        t["grad"] = torch.ones(3, 16, device="cuda")
+        t["row_ids"] = torch.tensor(ids, device="cuda")
+        t["n_rows"] = torch.tensor([n], device="cuda")
+        old, ws = _copy(t), _ws(256)
+        H.hstu_adamw_step(H.AdamWTensors([t]), ws, step=1, **HYPER)
+        assert H.hstu_read_status(ws) == BAD_IDS, ids
+        changed = (t["param"] != old["param"]).any(1).nonzero().flatten().tolist()
+        assert changed == good, (ids, changed)
+        t["row_ids"].copy_(torch.tensor([0, 4, 9], device="cuda"))
+        t["n_rows"].fill_(3)
+        H.hstu_adamw_step(H.AdamWTensors([t]), ws, step=2, **HYPER)
+        assert H.hstu_read_status(ws) == 0
+
+
+def test_step_is_skipped_when_the_scale_is_not_finite():
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    for bits in (32, 8):
+        t = _make(1000, "bf16", "f32", True, bits, 2)
+        old, lst, ws = _copy(t), H.AdamWTensors([t]), _ws(256)
+        for x in (math.nan, math.inf, -math.inf):
+            H.hstu_adamw_step(lst, ws, step=1, lr=1.0, grad_scale=torch.tensor([x], device="cuda"))
+        zero = torch.zeros(1, dtype=torch.int64, device="cuda")
+        H.hstu_adamw_step(lst, ws, step=zero, lr=1.0)
+        assert H.hstu_read_status(ws) == INVALID
+        for k, x in old.items():
+            assert torch.equal(t[k], x)
+
+
+def test_not_finite_gradients_stay_in_their_element():
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    for bits in (32, 8):
+        t = _make(512, "f32", "f32", False, bits, 2)
+        t["grad"][7], t["grad"][300] = math.nan, math.inf
+        clean = _copy(t)
+        clean["grad"][7], clean["grad"][300] = 0, 0
+        ws = _ws(256)
+        H.hstu_adamw_step(H.AdamWTensors([t]), ws, step=3, seed=1, **HYPER)
+        H.hstu_adamw_step(H.AdamWTensors([clean]), ws, step=3, seed=1, **HYPER)
+        assert torch.isnan(t["param"][7]) and torch.isnan(t["param"][300])
+        keep = torch.ones(512, dtype=torch.bool, device="cuda")
+        keep[7] = keep[300] = False
+        for k in ("param", "m", "v"):
+            assert torch.equal(t[k][keep], clean[k][keep])
+        if bits == 8:
+            assert (t["m"][~keep] & 0x7F == 0x7F).all() and (t["v"][~keep] == 0x7F).all()
+
+
+def test_small_second_moments_keep_moving():
+    """v moves by 1e-3 of itself per step, far less than a code step s <= 2^-3 of
+    its root: under rounding to nearest it would stand still.  100 steps with
+    one gradient, then 1500 with none for half of the elements: their mean v
+    falls to 0.999^1500 = 0.22 of what it was.  The stored root r is right in
+    the mean; its variance, s^2 q (1 - q) r^2 per step for a move of q code
+    steps, biases v = r^2 upwards: while v grows linearly q = 1 / (2 t s), and
+    a bias of step t weighs t / 100 at step 100, so at most s / 2 = 6.3%; while
+    it falls q = 5e-4 / s, so at most 1500 * 5e-4 s = 9.4%; together (factors)
+    under 17%.  The mean over 2^15 elements with a spread of at most 100% adds
+    5 / 2^7.5 = 2.8%."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    n = 1 << 16
+    t = _make(n, "f32", "f32", False, 8, 0, zero=True)
+    t["grad"].fill_(0.5)
+    lst, ws = H.AdamWTensors([t]), _ws(256)
+    v = 0.0
+    for step in range(1, 1601):
+        if step == 101:
+            t["grad"][n // 2:] = 0.0
+        H.hstu_adamw_step(lst, ws, step=step, lr=1e-3, seed=17)
+        v = 0.999 * v + (0.001 * 0.25 if step <= 100 else 0.0)
+    scale = torch.exp2(t["v_scale"].float() - 127).repeat_interleave(256)
+    r = t["v"].view(torch.float8_e4m3fn).float() * scale
+    mean = float(r[n // 2:].double().square().mean())
+    assert -0.028 <= mean / v - 1 <= 0.20, (mean, v)
+
+
+def test_captured_step_reads_step_and_rate_from_the_device():
+    """A captured norm and step, replayed with a step counter, a rate and
+    gradients that change on the device, equals the eager steps."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    ts = [_make(n, "bf16", "f32", True, b, n) for n, b in ((5000, 32), (777, 8), (1, 32))]
+    eager = [_copy(t) for t in ts]
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    lr = torch.zeros(1, device="cuda")
+    out, out2 = torch.zeros(2, device="cuda"), torch.zeros(2, device="cuda")
+    nws, ws = _ws(H.hstu_grad_norm_workspace_size()), _ws(256)
+    lst, elst = H.AdamWTensors(ts), H.AdamWTensors(eager)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step += 1
+        H.hstu_grad_norm(lst, 0.5, out, nws)
+        H.hstu_adamw_step(lst, ws, lr=lr, step=step, grad_scale=out[1:], seed=4)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for k in range(1, 5):
+        lr.fill_(2.0 ** -k)
+        for a, b in zip(ts, eager):
+            a["grad"].normal_(generator=g)
+            b["grad"].copy_(a["grad"])
+        graph.replay()
+        H.hstu_grad_norm(elst, 0.5, out2, nws)
+        H.hstu_adamw_step(elst, ws, lr=2.0 ** -k, step=k, grad_scale=out2[1:], seed=4)
+        torch.cuda.synchronize()
+        assert H.hstu_read_status(ws) == 0 and torch.equal(out, out2)
+        for a, b in zip(ts, eager):
+            for q in a:
+                assert torch.equal(a[q], b[q]), q
+    del graph
+
+
+def test_offsets_past_32_bits():
+    """A table of more than 2^31 elements: its last rows."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    R, d = 2_200_000, 1024
+    z = lambda dt: torch.zeros(R, d, dtype=dt, device="cuda")  # noqa: E731
+    t = dict(param=z(torch.bfloat16), m=z(torch.uint8), v=z(torch.uint8),
+             m_scale=torch.zeros(R * 4, dtype=torch.uint8, device="cuda"),
+             v_scale=torch.zeros(R * 4, dtype=torch.uint8, device="cuda"),
+             grad=torch.ones(3, d, device="cuda"),
+             row_ids=torch.tensor([0, R - 2, R - 1], device="cuda"),
+             n_rows=torch.tensor([3], device="cuda"))
+    ws = _ws(256)
+    H.hstu_adamw_step(H.AdamWTensors([t]), ws, step=1, lr=0.5)
+    assert H.hstu_read_status(ws) == 0
+    want = torch.tensor(-0.5, dtype=torch.bfloat16)
+    for r in (0, R - 2, R - 1):
+        assert (t["param"][r] == want).all() and (t["m_scale"][4 * r:4 * r + 4] > 0).all()
+    assert not t["param"][1:R - 2].any() and not t["m"][1:R - 2].any()
