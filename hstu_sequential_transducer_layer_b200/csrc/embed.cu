@@ -15,9 +15,13 @@
 // memory, and the parts of one that passes a block's border through the
 // workspace (at most two partial rows per block), by k_embed_join.
 #include <cuda_bf16.h>
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "ptx.cuh"
 
@@ -28,6 +32,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortItems = 8;
 constexpr int kSortTile = kSortThreads * kSortItems;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxCluster = 16;
 constexpr int kDigitBits = 10;  // at most; bins of one pass
 constexpr int kMaxBins = 1 << kDigitBits;
 
@@ -229,6 +234,7 @@ struct SortArgs {
   uint32_t* hist;          // [tiles, bins] counts, then exclusive over tiles; [bins] totals behind
   int32_t* bad;            // per tile: an id outside the table was seen
   int32_t* heads;          // per tile: touched rows that start in it
+  int32_t* sums;           // one-launch sort: per block (bad id seen, heads, live, -)
   uint32_t* rank;          // per sorted position: its segment
   uint32_t* seg_start;     // per segment: its first sorted position
   int64_t* row_ids;        // compact form: the touched rows (else null)
@@ -301,19 +307,21 @@ __global__ void k_sort_scan(const SortArgs a, int pass) {
 }
 
 // Ranks a tile's items among those of the same digit, in tile order: each
-// warp counts its own 256 consecutive items (equal digits of one 32-item step
-// found by match), then the warps' counts are summed up per digit.  On return
-// hist[w][b] is the number of items of digit b in warps before w, and rank[k]
-// this thread's item's number inside its warp.
-DEVI void rank_tile(const uint32_t (&digit)[kSortItems], const bool (&in)[kSortItems], int bins,
-                    uint16_t* hist, uint32_t (&rank)[kSortItems]) {
+// warp counts its own 32 * items consecutive items (equal digits of one
+// 32-item step found by match), then the warps' counts are summed up per
+// digit.  On return hist[w][b] is the number of items of digit b in warps
+// before w, rank[k] this thread's item's number inside its warp, and total[b]
+// (if given) the tile's number of items of digit b.
+DEVI void rank_tile(const uint32_t (&digit)[kSortItems], const bool (&in)[kSortItems], int items,
+                    int bins, uint16_t* hist, uint32_t (&rank)[kSortItems], uint32_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * bins / 2; i += kSortThreads)
-    reinterpret_cast<uint32_t*>(hist)[i] = 0;
+  for (int i = threadIdx.x; i < kSortWarps * bins / 8; i += kSortThreads)
+    reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   uint16_t* mine = hist + warp * bins;
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
+    if (k >= items) break;
     const uint32_t d = in[k] ? digit[k] : 0xffffffffu;
     const uint32_t peers = __match_any_sync(0xffffffffu, d);
     const uint32_t before = in[k] ? mine[d] : 0;
@@ -323,13 +331,19 @@ DEVI void rank_tile(const uint32_t (&digit)[kSortItems], const bool (&in)[kSortI
     __syncwarp();
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+  // two digits per thread, as one 32-bit sum (a tile's counts fit 16 bits)
+  uint32_t* two = reinterpret_cast<uint32_t*>(hist);
+  for (int b = threadIdx.x; b < bins / 2; b += kSortThreads) {
     uint32_t sum = 0;
-#pragma unroll 8
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t n = hist[w * bins + b];
-      hist[w * bins + b] = (uint16_t)sum;
+      const uint32_t n = two[w * (bins / 2) + b];
+      two[w * (bins / 2) + b] = sum;
       sum += n;
+    }
+    if (total) {
+      total[2 * b] = sum & 0xffffu;
+      total[2 * b + 1] = sum >> 16;
     }
   }
   __syncthreads();
@@ -361,7 +375,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const SortArgs a,
     key[k] = in[k] ? src[i] : 0;
     digit[k] = (key[k] >> shift) & (bins - 1);
   }
-  rank_tile(digit, in, bins, s_warp_hist, rank);
+  rank_tile(digit, in, kSortItems, bins, s_warp_hist, rank, nullptr);
   uint32_t* dst_key = a.key[(pass + 1) & 1];
   uint32_t* dst_val = a.val[(pass + 1) & 1];
 #pragma unroll
@@ -432,6 +446,183 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_segments(const SortArgs a
   }
 }
 
+// ---------------------------------------------------------------- one-launch sort
+// Up to kClusterTokens tokens are sorted by one cluster of up to 16 blocks,
+// each holding its tile of (key, token) pairs in shared memory: a pass ranks
+// the tile, adds up the blocks' digit counts and writes every pair into the shared memory of the block that its
+// new position falls to.  The blocks' digit counts go through global memory: 16
+// blocks reading 1024 counts of each other are 64 KB per block, which took 10,300
+// cycles a pass as shared-memory reads across the cluster.  The barriers of a
+// pass are the cluster's own (they order global memory too), so the whole sort
+// with the segments' numbers is one launch.  The launch's other
+// clusters clear the dense gradient meanwhile (if there is one to clear): the
+// sort is bound by its barriers and leaves the memory idle.
+constexpr int64_t kClusterTokens = (int64_t)kMaxCluster * kSortTile;
+
+struct FillArgs {
+  uint8_t* out;        // null: nothing to clear
+  int64_t rows, row_bytes, pitch;
+  int unit;            // bytes of one element
+};
+
+DEVI void fill_zero(const FillArgs& f, int64_t block, int64_t blocks) {
+  if (f.row_bytes == f.pitch) {
+    const int64_t bytes = f.rows * f.row_bytes, n16 = bytes / 16;
+    uint4* q = reinterpret_cast<uint4*>(f.out);
+    for (int64_t i = block * kSortThreads + threadIdx.x; i < n16; i += blocks * kSortThreads)
+      q[i] = make_uint4(0, 0, 0, 0);
+    if (block == 0 && threadIdx.x < 16 && n16 * 16 + threadIdx.x < bytes)
+      f.out[n16 * 16 + threadIdx.x] = 0;
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t r = block * kSortWarps + warp; r < f.rows; r += blocks * kSortWarps) {
+    uint8_t* row = f.out + r * f.pitch;
+    for (int64_t c = (int64_t)lane * f.unit; c < f.row_bytes; c += 32 * f.unit) {
+      if (f.unit == 4)
+        *reinterpret_cast<uint32_t*>(row + c) = 0;
+      else
+        *reinterpret_cast<uint16_t*>(row + c) = 0;
+    }
+  }
+}
+
+size_t cluster_smem(int tile, int bins) {
+  return (size_t)tile * 16 + (size_t)kSortWarps * bins * 2 + (size_t)bins * 4;
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    k_embed_sort(const SortArgs a, const FillArgs f, int tile) {
+  namespace cg = cooperative_groups;
+  extern __shared__ uint4 s_mem[];
+  __shared__ int s_scan[kSortWarps];
+  __shared__ int s_before;
+  grid_dep_launch();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nc = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
+  if ((int)blockIdx.x >= nc) {
+    fill_zero(f, (int64_t)blockIdx.x - nc, (int64_t)gridDim.x - nc);
+    return;
+  }
+  const int bins = 1 << a.digit;
+  uint2* pair = reinterpret_cast<uint2*>(s_mem);  // (key, token)
+  uint2* pair2 = pair + tile;
+  uint16_t* hist = reinterpret_cast<uint16_t*>(pair2 + tile);
+  uint32_t* base = reinterpret_cast<uint32_t*>(hist + kSortWarps * bins);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = min(max(a.T - c * tile, 0), tile);
+  const int items = (tile + kSortThreads - 1) / kSortThreads;
+  const int w0 = warp * 32 * items + lane;  // this thread's items: w0 + 32 k
+  uint2 x[kSortItems];
+  bool in[kSortItems];
+  bool bad = false;
+  {
+    int64_t id[kSortItems];
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      in[k] = k < items && w0 + 32 * k < n;
+      id[k] = in[k] ? a.ids[c * tile + w0 + 32 * k] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      bool b;
+      x[k] = make_uint2(token_key(a, id[k], &b), (uint32_t)(c * tile + w0 + 32 * k));
+      bad |= in[k] && b;
+    }
+  }
+  for (int p = 0; p < a.passes; ++p) {
+    uint32_t digit[kSortItems], rank[kSortItems];
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      if (p > 0) x[k] = in[k] ? pair[w0 + 32 * k] : make_uint2(0, 0);
+      digit[k] = (x[k].x >> (p * a.digit)) & (bins - 1);
+    }
+    rank_tile(digit, in, items, bins, hist, rank, a.hist + c * bins);
+    cluster.sync();  // every block's totals
+    uint32_t before = 0, all = 0;
+    if (tid < bins) {
+      uint32_t t[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        t[r] = r < nc ? __ldcg(a.hist + r * bins + tid) : 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        all += t[r];
+        before += r < c ? t[r] : 0;
+      }
+    }
+    int sum;
+    const int first = block_excl_scan<kSortThreads>((int)all, s_scan, &sum);
+    if (tid < bins) base[tid] = (uint32_t)first + before;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      if (!in[k]) continue;
+      const uint32_t to = base[digit[k]] + hist[warp * bins + digit[k]] + rank[k];
+      const uint32_t r = to / (uint32_t)tile;
+      cluster.map_shared_rank(pair2, (int)r)[to - r * (uint32_t)tile] = x[k];
+    }
+    cluster.sync();  // every pair has arrived
+    uint2* t = pair;
+    pair = pair2;
+    pair2 = t;
+  }
+  // segments: this thread's `items` consecutive sorted positions
+  const uint32_t left = c > 0 && n > 0 ? cluster.map_shared_rank(pair, c - 1)[tile - 1].x : 0;
+  const int i0 = tid * items;
+  int count = 0;  // heads in the low half, live tokens in the high half
+  for (int k = 0; k < items; ++k) {
+    const int i = i0 + k;
+    if (i >= n) break;
+    const uint32_t key = pair[i].x;
+    const bool first = c == 0 && i == 0;
+    if (key < a.n_rows)
+      count += 0x10000 + (first || (i > 0 ? pair[i - 1].x : left) != key);
+  }
+  int all;
+  int seg = block_excl_scan<kSortThreads>(count, s_scan, &all) & 0xffff;
+  const int any_bad = __syncthreads_or(bad);
+  if (tid == 0) *reinterpret_cast<int4*>(a.sums + 4 * c) = make_int4(any_bad, all & 0xffff, all >> 16, 0);
+  cluster.sync();  // the blocks' sums; also the last access to another block's shared memory is done
+  if (warp == 0) {
+    const int4 o = lane < nc ? __ldcg(reinterpret_cast<const int4*>(a.sums) + lane)
+                             : make_int4(0, 0, 0, 0);
+    const int before = __reduce_add_sync(0xffffffffu, lane < c ? o.y : 0);
+    const int bads = __reduce_add_sync(0xffffffffu, o.x);
+    const int heads = __reduce_add_sync(0xffffffffu, o.y);
+    const int live = __reduce_add_sync(0xffffffffu, o.z);
+    if (lane == 0) {
+      s_before = before;
+      if (c == 0) {
+        a.head->status = bads ? HSTU_ERR_BAD_IDS : HSTU_OK;
+        a.head->live = live;
+        a.head->segs = heads;
+        if (a.n_unique) *a.n_unique = heads;
+      }
+    }
+  }
+  __syncthreads();
+  seg += s_before;
+  uint32_t* out_key = a.key[a.passes & 1] + c * tile;
+  uint32_t* out_val = a.val[a.passes & 1] + c * tile;
+  for (int i = tid; i < n; i += kSortThreads) {
+    out_key[i] = pair[i].x;
+    out_val[i] = pair[i].y;
+  }
+  for (int k = 0; k < items; ++k) {
+    const int i = i0 + k;
+    if (i >= n) break;
+    const uint32_t key = pair[i].x;
+    if (key >= a.n_rows) break;
+    if ((c == 0 && i == 0) || (i > 0 ? pair[i - 1].x : left) != key) {
+      a.seg_start[seg] = (uint32_t)(c * tile + i);
+      if (a.row_ids) a.row_ids[seg] = (int64_t)key;
+      ++seg;
+    }
+    a.rank[c * tile + i] = (uint32_t)(seg - 1);
+  }
+}
+
 // ---------------------------------------------------------------- sums
 struct SumArgs {
   const SortHead* head;
@@ -499,7 +690,7 @@ DEVI void add8(const float* p, int lane, float (&f)[8]) {
 }
 
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kRunWarps * 32) k_embed_sum(const SumArgs a) {
+__global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const SumArgs a) {
   __shared__ float s_pre[kRunWarps][kColumns], s_post[kRunWarps][kColumns];
   __shared__ int s_flags[kRunWarps];  // 1: pre holds a part, 2: it goes on past this warp
   grid_dep_launch();
@@ -534,25 +725,19 @@ __global__ void __launch_bounds__(kRunWarps * 32) k_embed_sum(const SumArgs a) {
     bool open = cur == prev;  // the running segment began before this warp's positions
     constexpr int kBatch = DT == HSTU_FP32 ? 4 : 8;
     for (int i0 = 0; i0 < n; i0 += kBatch) {
-      float x[kBatch][8];
-      if (VEC) {
-        Raw8<DT> r[kBatch];
+      Raw8<DT> r[VEC ? kBatch : 1];
+      float one[VEC ? 1 : kBatch][8];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t t = __shfl_sync(0xffffffffu, val, (i0 + u) & 31);
+        if (VEC) {
           r[u] = Raw8<DT>{};
-          const int64_t t = __shfl_sync(0xffffffffu, val, (i0 + u) & 31);
           if (i0 + u < n && c0 + 8 * lane < a.d) load8(r[u], a.dY, t * a.ld_dy + c0 + 8 * lane);
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) widen(r[u], x[u]);
-      } else {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int64_t t = __shfl_sync(0xffffffffu, val, (i0 + u) & 31);
+        } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int c = c0 + 32 * j + lane;
-            x[u][j] = i0 + u < n && c < a.d ? load1<DT>(a.dY, t * a.ld_dy + c) : 0.f;
+            one[u][j] = i0 + u < n && c < a.d ? load1<DT>(a.dY, t * a.ld_dy + c) : 0.f;
           }
         }
       }
@@ -573,8 +758,10 @@ __global__ void __launch_bounds__(kRunWarps * 32) k_embed_sum(const SumArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = 0.f;
           }
+          float x[8];
+          if (VEC) widen(r[u], x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] += x[u][j];
+          for (int j = 0; j < 8; ++j) acc[j] += VEC ? x[j] : one[u][j];
         }
       }
     }
@@ -657,7 +844,7 @@ bool dtype_ok(int32_t t) { return t == HSTU_BF16 || t == HSTU_FP32 || t == HSTU_
 size_t dsize(int32_t t) { return t == HSTU_FP32 ? 4 : 2; }
 
 struct BwdLayout {
-  size_t head, key[2], val[2], hist, bad, heads, rank, seg_start, part, total;
+  size_t head, key[2], val[2], hist, bad, heads, sums, rank, seg_start, part, total;
   int tiles, passes, digit, runs, ld_part;
 };
 
@@ -681,7 +868,8 @@ bool bwd_layout(int64_t T, int64_t R, int32_t d, BwdLayout* L) {
     L->key[i] = take((size_t)T * 4);
     L->val[i] = take((size_t)T * 4);
   }
-  L->hist = take(((size_t)L->tiles + 1) * 4 << L->digit);
+  L->hist = take((size_t)std::max(L->tiles + 1, kMaxCluster) * 4 << L->digit);
+  L->sums = take(kMaxCluster * 16);
   L->bad = take((size_t)L->tiles * 4);
   L->heads = take((size_t)L->tiles * 4);
   L->rank = take((size_t)T * 4);
@@ -729,6 +917,73 @@ cudaError_t sort_tokens(const SortArgs& a, cudaStream_t s) {
   return e;
 }
 
+// Blocks of the sort's cluster: a power of two with at least 1024 tokens each
+// where there are so many (a block's pass costs about the same for 1 to 1024
+// tokens).
+int cluster_blocks(int64_t T) {
+  int n = 1;
+  while (n < kMaxCluster && (int64_t)n * kSortThreads < T) n *= 2;
+  return n;
+}
+
+// Whether clusters of `blocks` blocks with this much shared memory fit the
+// current device (asked once per device and size).
+bool cluster_fits(int blocks, size_t smem, const cudaLaunchConfig_t& cfg) {
+  static std::mutex mu;
+  static std::map<std::pair<int, std::pair<int, size_t>>, bool> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_pair(dev, std::make_pair(blocks, smem));
+  const auto it = known.find(key);
+  if (it != known.end()) return it->second;
+  const void* fn = reinterpret_cast<const void*>(k_embed_sort);
+  int n = 0;
+  bool ok = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+            cudaSuccess;
+  ok = ok && cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
+  if (!ok) cudaGetLastError();
+  known[key] = ok;
+  return ok;
+}
+
+// The one-launch sort; *done = false if this device cannot run it.
+cudaError_t sort_tokens_cluster(const SortArgs& a, const FillArgs& f, cudaStream_t s, bool* done) {
+  const int nc = cluster_blocks(a.T), bins = 1 << a.digit;
+  const int tile = ((a.T + nc - 1) / nc + 31) / 32 * 32;
+  const size_t smem = cluster_smem(tile, bins);
+  *done = false;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(k_embed_sort), (int)smem);
+  if (e != cudaSuccess) return e;
+  int fill = 0;  // clusters that clear the gradient, 64 KB or more for each of their blocks
+  if (f.out) {
+    const int64_t bytes = f.rows * f.row_bytes;
+    fill = (int)std::min<int64_t>((bytes + 65535) / 65536 / nc + 1, num_sms() / nc - 1);
+    fill = std::max(fill, 1);
+  }
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)nc;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(nc * (1 + fill)));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (!cluster_fits(nc, smem, cfg)) return cudaSuccess;
+  *done = true;
+  LaunchScope ls(K_EMBED_SORT, s);
+  return cudaLaunchKernelEx(&cfg, k_embed_sort, a, f, tile);
+}
+
+cudaError_t clear_rows(const FillArgs& f, cudaStream_t s) {
+  return f.row_bytes == f.pitch
+             ? cudaMemsetAsync(f.out, 0, (size_t)(f.rows * f.row_bytes), s)
+             : cudaMemset2DAsync(f.out, (size_t)f.pitch, 0, (size_t)f.row_bytes, (size_t)f.rows, s);
+}
+
 template <int DT>
 cudaError_t sum_rows(const SumArgs& a, int runs, bool vec, cudaStream_t s) {
   const dim3 grid((unsigned)runs, (unsigned)((a.d + kColumns - 1) / kColumns));
@@ -764,14 +1019,17 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
   if (!ws || ws_bytes < L.total || !al256(ws)) return HSTU_ERR_WORKSPACE;
   auto at = [&](size_t o) { return static_cast<uint8_t*>(ws) + o; };
   SortHead* head = reinterpret_cast<SortHead*>(at(L.head));
+  FillArgs f{};
   if (!compact && !accumulate) {
-    const size_t row = (size_t)d * dsize(out_dt), pitch = (size_t)ld_out * dsize(out_dt);
-    const cudaError_t e = row == pitch ? cudaMemsetAsync(out, 0, (size_t)R * row, s)
-                                       : cudaMemset2DAsync(out, pitch, 0, row, (size_t)R, s);
-    if (e != cudaSuccess) return cuda_status(e, "embed_bwd: clearing the gradient");
+    f.out = static_cast<uint8_t*>(out);
+    f.rows = R;
+    f.unit = (int)dsize(out_dt);
+    f.row_bytes = (int64_t)d * f.unit;
+    f.pitch = ld_out * f.unit;
   }
   if (T == 0) {
     cudaError_t e = cudaMemsetAsync(head, 0, sizeof(SortHead), s);
+    if (e == cudaSuccess && f.out) e = clear_rows(f, s);
     if (e == cudaSuccess && compact) e = cudaMemsetAsync(n_unique, 0, 8, s);
     return cuda_status(e, "embed_bwd: empty batch");
   }
@@ -790,12 +1048,19 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
   q.hist = reinterpret_cast<uint32_t*>(at(L.hist));
   q.bad = reinterpret_cast<int32_t*>(at(L.bad));
   q.heads = reinterpret_cast<int32_t*>(at(L.heads));
+  q.sums = reinterpret_cast<int32_t*>(at(L.sums));
   q.rank = reinterpret_cast<uint32_t*>(at(L.rank));
   q.seg_start = reinterpret_cast<uint32_t*>(at(L.seg_start));
   q.row_ids = compact ? row_ids : nullptr;
   q.n_unique = compact ? n_unique : nullptr;
   q.head = head;
-  cudaError_t e = sort_tokens(q, s);
+  cudaError_t e = cudaSuccess;
+  bool sorted = false;
+  if (T <= kClusterTokens) e = sort_tokens_cluster(q, f, s, &sorted);
+  if (e == cudaSuccess && !sorted) {
+    if (f.out) e = clear_rows(f, s);
+    if (e == cudaSuccess) e = sort_tokens(q, s);
+  }
   if (e != cudaSuccess) return cuda_status(e, "embed_bwd: sort");
   SumArgs a{};
   a.head = head;
