@@ -21,7 +21,7 @@ namespace {
 constexpr int kBlockElems = HSTU_STATE_BLOCK;
 constexpr int kChunkBlocks = 8;  // one per warp
 constexpr int kThreads = 32 * kChunkBlocks;
-// Tensors of one launch: 120 bytes each in 32,764 bytes of kernel parameters.
+// Tensors of one launch: 120 bytes each, in 32,764 bytes of kernel parameters.
 constexpr int kMaxTensors = 256;
 
 // ---------------------------------------------------------------- gradient norm
@@ -158,6 +158,7 @@ struct StepTensor {
   const int64_t* row_ids;  // row-sparse, else null
   const int64_t* n_rows;
   int64_t n;               // elements of the parameter
+  int64_t rows;            // row-sparse: rows of the table
   int32_t row_len, row_blocks, max_rows;
   int32_t chunk0;          // first chunk of this tensor
   float weight_decay;
@@ -169,7 +170,7 @@ struct StepArgs {
   int n, first;            // tensors of this launch; number of the first one in the caller's list
   int64_t chunks;
   float b1, omb1, b2, omb2, eps;
-  double log_b1, log_b2, lr;
+  double log_b1, log_b2, bc1, bc2, lr;
   int64_t step;
   const int64_t* step_dev;
   const float* lr_dev;
@@ -179,6 +180,8 @@ struct StepArgs {
   int set_ok;              // nothing in this call can fail on the device: block 0 writes HSTU_OK
 };
 
+static_assert(sizeof(StepArgs) <= 32764, "kernel parameters");
+
 // The 32-bit integer mix of C. Wellons' hash prospector ("lowbias32").
 DEVI uint32_t mix32(uint32_t x) {
   x ^= x >> 16;
@@ -187,6 +190,7 @@ DEVI uint32_t mix32(uint32_t x) {
   x *= 0x846ca68bu;
   return x ^ (x >> 16);
 }
+constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
 // SplitMix64's output mix (Steele, Lea and Flood, OOPSLA 2014).
 DEVI uint64_t split_mix(uint64_t z) {
   z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
@@ -194,65 +198,55 @@ DEVI uint64_t split_mix(uint64_t z) {
   return z ^ (z >> 31);
 }
 
-// e4m3 code of the magnitude t (scaled, below 2^8 or not finite), rounded up
-// when the 16-bit number r reaches the missing part: an e4m3 code step is
-// 2^20 units of fp32's significand, so r * 16 is added and the rest cut.
-// Below 2^-6 the codes have a fixed step, which adding 2^-6 gives them.
-DEVI uint32_t e4m3_up(float t, uint32_t r16) {
+// e4m3 code of the magnitude t (scaled, below 2^8), rounded up when the
+// 16-bit number r / 2^16 reaches the missing part: an e4m3 code step is 2^20
+// units of fp32's significand, so r * 16 is added and the rest cut.  Below
+// 2^-6 the codes have a fixed step, which adding 2^-6 gives them.  r20 is r
+// shifted left by 4, below 2^20.
+DEVI uint32_t e4m3_up(float t, uint32_t r20) {
   const bool sub = t < 0.015625f;
   t = sub ? __fadd_rn(t, 0.015625f) : t;
-  const uint32_t c = ((__float_as_uint(t) + (r16 << 4)) >> 20) - (sub ? 968u : 960u);
-  return t <= 512.f ? c : 0x7fu;  // NaN and infinity: NaN
+  return (__float_as_uint(t) + r20 - (sub ? 968u << 20 : 960u << 20)) >> 20;
 }
 DEVI float2 e4m3x2_to_f32(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-DEVI float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;
-}
-// Scale byte of a block whose largest finite magnitude is `top`: 2^(byte - 127)
-// puts it into [2^7, 2^8), half of e4m3's range, so rounding up never
-// saturates.
-DEVI int scale_byte(float top) { return max(1, (int)(__float_as_uint(top) >> 23) - 7); }
+constexpr uint32_t kInfBits = 0x7f800000u;
+DEVI uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// Scale byte of a block whose largest finite magnitude has these bits:
+// 2^(byte - 127) puts it into [2^7, 2^8), half of e4m3's range, so rounding up
+// never saturates.
+DEVI int scale_byte(uint32_t top) { return max(1, (int)(top >> 23) - 7); }
 
-// Four consecutive elements as fp32.
-DEVI void load4(int dtype, const void* p, int64_t i, float (&f)[4]) {
+// Four consecutive elements as they lie in memory (16-bit types: x and y).
+DEVI uint4 raw4(bool wide, const uint8_t* p, int e) {
+  if (wide) return *reinterpret_cast<const uint4*>(p + 4 * e);
+  const uint2 w = *reinterpret_cast<const uint2*>(p + 2 * e);
+  return make_uint4(w.x, w.y, 0, 0);
+}
+DEVI void widen4(int dtype, const uint4& r, float (&f)[4]) {
   if (dtype == HSTU_FP32) {
-    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
+    f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y);
+    f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
+  } else if (dtype == HSTU_BF16) {
+    f[0] = __uint_as_float(r.x << 16), f[1] = __uint_as_float(r.x & 0xffff0000u);
+    f[2] = __uint_as_float(r.y << 16), f[3] = __uint_as_float(r.y & 0xffff0000u);
   } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-    if (dtype == HSTU_BF16) {
-      f[0] = __uint_as_float(w.x << 16), f[1] = __uint_as_float(w.x & 0xffff0000u);
-      f[2] = __uint_as_float(w.y << 16), f[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-      f[0] = x.x, f[1] = x.y, f[2] = y.x, f[3] = y.y;
-    }
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+    f[0] = x.x, f[1] = x.y, f[2] = y.x, f[3] = y.y;
   }
 }
+DEVI uint32_t bits2(const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); }
+DEVI uint32_t bits2(const __half2& x) { return *reinterpret_cast<const uint32_t*>(&x); }
 // What storing x in `dtype` leaves of it.
 DEVI float rounded(int dtype, float x) {
   return dtype == HSTU_FP32   ? x
          : dtype == HSTU_BF16 ? __bfloat162float(__float2bfloat16_rn(x))
                               : __half2float(__float2half_rn(x));
 }
-DEVI void store4(int dtype, void* p, int64_t i, const float (&f)[4]) {
-  if (dtype == HSTU_FP32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
-  } else if (dtype == HSTU_BF16) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  } else {
-    const __half2 x = __floats2half2_rn(f[0], f[1]), y = __floats2half2_rn(f[2], f[3]);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  }
-}
+DEVI __half half_sat(float x) { return __float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)); }
 DEVI void store_elem(int dtype, void* p, int64_t i, float x) {
   if (dtype == HSTU_FP32)
     static_cast<float*>(p)[i] = x;
@@ -262,12 +256,271 @@ DEVI void store_elem(int dtype, void* p, int64_t i, float x) {
     static_cast<__half*>(p)[i] = __float2half_rn(x);
 }
 
-// One step of every tensor.  A warp takes a block of 256 elements; lane l
-// holds elements 4 l + 128 j + (0..3), j = 0, 1, so every access of a warp is
-// to consecutive addresses.  Bandwidth-bound: per element the gradient, the
-// states and the (master) parameter are read once and the results written
-// once; all of a lane's loads are issued before the first one is used.
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ StepArgs a) {
+// What all elements of a step share.
+struct StepConst {
+  float b1, omb1, b2, omb2, eps, gs, step_size, rbc2, decay;
+};
+
+// One element: m, v and p after the step, root = sqrt(v).  The moments'
+// products and sums are kept apart (no contraction), so that an 8-bit state
+// does not depend on how the compiler fuses them.
+DEVI void step_elem(const StepConst& k, float g, float& m, float& v, float& p, float& root) {
+  g = __fmul_rn(g, k.gs);
+  m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.omb1));
+  v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.omb2));
+  root = __fsqrt_rn(v);
+  const float u = __fdividef(m, fmaf(root, k.rbc2, k.eps));
+  p -= fmaf(p, k.decay, u * k.step_size);
+}
+
+// Key of a block's random numbers.
+DEVI uint32_t block_key(uint64_t key, int64_t block) {
+  return mix32(mix32((uint32_t)block ^ (uint32_t)key) ^ (uint32_t)((uint64_t)block >> 32) ^
+               (uint32_t)(key >> 32));
+}
+DEVI uint32_t elem_random(uint32_t base, int e) { return mix32(base + (uint32_t)e * 0x9E3779B9u); }
+
+// Four codes of each state, element e0 the first.  CHECK: some value is not
+// finite; those become NaN.
+template <bool CHECK>
+DEVI void encode4(const float (&m)[4], const float (&root)[4], float mi, float vi, uint32_t base,
+                  int e0, uint32_t& mc, uint32_t& vc) {
+  mc = vc = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t r = elem_random(base, e0 + i);
+    uint32_t a = e4m3_up(fabsf(m[i]) * mi, (r << 4) & 0xffff0u);
+    uint32_t b = e4m3_up(root[i] * vi, (r >> 12) & 0xffff0u);
+    if (CHECK) {
+      a = abs_bits(m[i]) < kInfBits ? a : 0x7fu;
+      b = abs_bits(root[i]) < kInfBits ? b : 0x7fu;
+    }
+    a |= (__float_as_uint(m[i]) >> 24) & 0x80u;
+    mc |= a << (8 * i);
+    vc |= b << (8 * i);
+  }
+}
+
+// Where a block of up to 256 elements lies.
+struct BlockAt {
+  int64_t g0, p0, block;  // first gradient and parameter element, block number in the tensor
+  int len;
+};
+
+// The step of one block whose length is a multiple of 4 and whose rows are
+// 16-byte aligned.  Lane l holds elements 4 l + 128 j + (0..3), j = 0, 1, so
+// every access of a warp is to consecutive addresses; all of a lane's loads
+// are issued before the first one is used.
+template <bool S8>
+DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k, uint64_t key) {
+  const int lane = threadIdx.x & 31;
+  const bool gw = q.grad_dtype == HSTU_FP32;
+  const bool pw = q.master || q.param_dtype == HSTU_FP32;
+  const uint8_t* gp = static_cast<const uint8_t*>(q.grad) + (at.g0 << (gw ? 2 : 1));
+  uint8_t* wp = q.master ? reinterpret_cast<uint8_t*>(q.master + at.p0)
+                         : static_cast<uint8_t*>(q.param) + (at.p0 << (pw ? 2 : 1));
+  uint8_t* mp = static_cast<uint8_t*>(q.m) + (S8 ? at.p0 : 4 * at.p0);
+  uint8_t* vp = static_cast<uint8_t*>(q.v) + (S8 ? at.p0 : 4 * at.p0);
+  uint4 gr[2], pr[2];
+  float m[2][4], v[2][4], p[2][4], root[2][4];
+  uint32_t mc[2], vc[2];
+  float ms = 0.f, vs = 0.f;
+  bool in[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = 4 * lane + 128 * j;
+    in[j] = e < at.len;
+    gr[j] = pr[j] = make_uint4(0, 0, 0, 0);
+    mc[j] = vc[j] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[j][i] = v[j][i] = 0.f;
+    if (in[j]) {
+      gr[j] = raw4(gw, gp, e);
+      pr[j] = raw4(pw, wp, e);
+      if (S8) {
+        mc[j] = *reinterpret_cast<const uint32_t*>(mp + e);
+        vc[j] = *reinterpret_cast<const uint32_t*>(vp + e);
+      } else {
+        widen4(HSTU_FP32, raw4(true, mp, e), m[j]);
+        widen4(HSTU_FP32, raw4(true, vp, e), v[j]);
+      }
+    }
+  }
+  if (S8) {
+    ms = __uint_as_float((uint32_t)q.m_scale[at.block] << 23);
+    vs = __uint_as_float((uint32_t)q.v_scale[at.block] << 23);
+  }
+  uint32_t top_m = 0, top_r = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float g[4];
+    widen4(q.grad_dtype, gr[j], g);
+    widen4(pw ? HSTU_FP32 : q.param_dtype, pr[j], p[j]);
+    if (S8) {
+      const float2 m0 = e4m3x2_to_f32(mc[j] & 0xffffu), m1 = e4m3x2_to_f32(mc[j] >> 16);
+      const float2 v0 = e4m3x2_to_f32(vc[j] & 0xffffu), v1 = e4m3x2_to_f32(vc[j] >> 16);
+      m[j][0] = m0.x, m[j][1] = m0.y, m[j][2] = m1.x, m[j][3] = m1.y;
+      v[j][0] = v0.x, v[j][1] = v0.y, v[j][2] = v1.x, v[j][3] = v1.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (S8) {
+        m[j][i] = __fmul_rn(m[j][i], ms);
+        v[j][i] = __fmul_rn(v[j][i], vs);
+        v[j][i] = __fmul_rn(v[j][i], v[j][i]);
+      }
+      step_elem(k, g[i], m[j][i], v[j][i], p[j][i], root[j][i]);
+      if (S8) {
+        top_m = max(top_m, abs_bits(m[j][i]));
+        top_r = max(top_r, abs_bits(root[j][i]));
+      }
+    }
+  }
+  if (S8) {
+    top_m = __reduce_max_sync(0xffffffffu, top_m);
+    top_r = __reduce_max_sync(0xffffffffu, top_r);
+    const bool odd = top_m >= kInfBits || top_r >= kInfBits;  // the same for the whole warp
+    if (odd) {
+      top_m = top_r = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a = abs_bits(m[j][i]), b = abs_bits(root[j][i]);
+          top_m = max(top_m, a < kInfBits ? a : 0);
+          top_r = max(top_r, b < kInfBits ? b : 0);
+        }
+      }
+      top_m = __reduce_max_sync(0xffffffffu, top_m);
+      top_r = __reduce_max_sync(0xffffffffu, top_r);
+    }
+    const int mb = scale_byte(top_m), vb = scale_byte(top_r);
+    const float mi = __uint_as_float((uint32_t)(254 - mb) << 23);
+    const float vi = __uint_as_float((uint32_t)(254 - vb) << 23);
+    const uint32_t base = block_key(key, at.block);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (odd)
+        encode4<true>(m[j], root[j], mi, vi, base, 4 * lane + 128 * j, mc[j], vc[j]);
+      else
+        encode4<false>(m[j], root[j], mi, vi, base, 4 * lane + 128 * j, mc[j], vc[j]);
+    }
+    if (lane == 0) {
+      q.m_scale[at.block] = (uint8_t)mb;
+      q.v_scale[at.block] = (uint8_t)vb;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (!in[j]) continue;
+    const int e = 4 * lane + 128 * j;
+    if (S8) {
+      *reinterpret_cast<uint32_t*>(mp + e) = mc[j];
+      *reinterpret_cast<uint32_t*>(vp + e) = vc[j];
+    } else {
+      *reinterpret_cast<float4*>(mp + 4 * e) = make_float4(m[j][0], m[j][1], m[j][2], m[j][3]);
+      *reinterpret_cast<float4*>(vp + 4 * e) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+    }
+    if (pw) *reinterpret_cast<float4*>(wp + 4 * e) = make_float4(p[j][0], p[j][1], p[j][2], p[j][3]);
+    __half2 h0, h1;  // the fp16 copy, of the stored value
+    if (q.param_dtype == HSTU_BF16) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(p[j][0], p[j][1]);
+      const __nv_bfloat162 y = __floats2bfloat162_rn(p[j][2], p[j][3]);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(q.param) + at.p0 + e) =
+          make_uint2(bits2(x), bits2(y));
+      if (q.copy) {
+        const float2 a = __bfloat1622float2(x), b = __bfloat1622float2(y);
+        h0 = __halves2half2(half_sat(a.x), half_sat(a.y));
+        h1 = __halves2half2(half_sat(b.x), half_sat(b.y));
+      }
+    } else if (q.param_dtype == HSTU_FP16) {
+      const __half2 x = __floats2half2_rn(p[j][0], p[j][1]);
+      const __half2 y = __floats2half2_rn(p[j][2], p[j][3]);
+      *reinterpret_cast<uint2*>(static_cast<__half*>(q.param) + at.p0 + e) =
+          make_uint2(bits2(x), bits2(y));
+      if (q.copy) {
+        const float2 a = __half22float2(x), b = __half22float2(y);
+        h0 = __halves2half2(half_sat(a.x), half_sat(a.y));
+        h1 = __halves2half2(half_sat(b.x), half_sat(b.y));
+      }
+    } else if (q.copy) {
+      h0 = __halves2half2(half_sat(p[j][0]), half_sat(p[j][1]));
+      h1 = __halves2half2(half_sat(p[j][2]), half_sat(p[j][3]));
+    }
+    if (q.copy)
+      *reinterpret_cast<uint2*>(q.copy + at.p0 + e) = make_uint2(bits2(h0), bits2(h1));
+  }
+}
+
+// The same for any other block (the end of a tensor, rows that are not
+// multiples of 4 elements), element by element: lane l takes elements l + 32 i.
+DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst& k, uint64_t key) {
+  const int lane = threadIdx.x & 31;
+  const void* wide = q.master ? static_cast<const void*>(q.master) : q.param;
+  const int wide_dt = q.master ? HSTU_FP32 : q.param_dtype;
+  float ms = 0.f, vs = 0.f, m[8], root[8];
+  if (q.state8) {
+    ms = __uint_as_float((uint32_t)q.m_scale[at.block] << 23);
+    vs = __uint_as_float((uint32_t)q.v_scale[at.block] << 23);
+  }
+  uint32_t top_m = 0, top_r = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane + 32 * i;
+    m[i] = root[i] = 0.f;
+    if (e >= at.len) continue;
+    const int64_t x = at.p0 + e;
+    float v, p = load_elem(wide_dt, wide, x);
+    const float g = load_elem(q.grad_dtype, q.grad, at.g0 + e);
+    if (q.state8) {
+      m[i] = __fmul_rn(e4m3x2_to_f32(static_cast<uint8_t*>(q.m)[x]).x, ms);
+      v = __fmul_rn(e4m3x2_to_f32(static_cast<uint8_t*>(q.v)[x]).x, vs);
+      v = __fmul_rn(v, v);
+    } else {
+      m[i] = static_cast<float*>(q.m)[x];
+      v = static_cast<float*>(q.v)[x];
+    }
+    step_elem(k, g, m[i], v, p, root[i]);
+    if (!q.state8) {
+      static_cast<float*>(q.m)[x] = m[i];
+      static_cast<float*>(q.v)[x] = v;
+    }
+    if (q.master) q.master[x] = p;
+    store_elem(q.param_dtype, q.param, x, p);
+    if (q.copy) q.copy[x] = half_sat(rounded(q.param_dtype, p));
+    const uint32_t a = abs_bits(m[i]), b = abs_bits(root[i]);
+    top_m = max(top_m, a < kInfBits ? a : 0);
+    top_r = max(top_r, b < kInfBits ? b : 0);
+  }
+  if (!q.state8) return;
+  const int mb = scale_byte(__reduce_max_sync(0xffffffffu, top_m));
+  const int vb = scale_byte(__reduce_max_sync(0xffffffffu, top_r));
+  const float mi = __uint_as_float((uint32_t)(254 - mb) << 23);
+  const float vi = __uint_as_float((uint32_t)(254 - vb) << 23);
+  const uint32_t base = block_key(key, at.block);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane + 32 * i;
+    if (e >= at.len) continue;
+    const uint32_t r = elem_random(base, e);
+    const uint32_t a = abs_bits(m[i]) < kInfBits ? e4m3_up(fabsf(m[i]) * mi, (r << 4) & 0xffff0u)
+                                                 : 0x7fu;
+    const uint32_t b = abs_bits(root[i]) < kInfBits ? e4m3_up(root[i] * vi, (r >> 12) & 0xffff0u)
+                                                    : 0x7fu;
+    static_cast<uint8_t*>(q.m)[at.p0 + e] =
+        (uint8_t)(a | ((__float_as_uint(m[i]) >> 24) & 0x80u));
+    static_cast<uint8_t*>(q.v)[at.p0 + e] = (uint8_t)b;
+  }
+  if (lane == 0) {
+    q.m_scale[at.block] = (uint8_t)mb;
+    q.v_scale[at.block] = (uint8_t)vb;
+  }
+}
+
+// One step of every tensor, a warp per block of 256 elements.
+// Bandwidth-bound: per element the gradient, the states and the (master)
+// parameter are read once and the results written once.
+__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ StepArgs a) {
   __shared__ float s_lr, s_step_size, s_rbc2;
   __shared__ int s_skip;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -275,9 +528,11 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Step
     const int64_t step = a.step_dev ? *a.step_dev : a.step;
     const float gs = a.grad_scale ? *a.grad_scale : 1.f;
     const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
-    // 1 - b^t without cancellation
-    s_step_size = (float)(lr / -expm1((double)step * a.log_b1));
-    s_rbc2 = (float)(1.0 / sqrt(-expm1((double)step * a.log_b2)));
+    // 1 - b^t without cancellation; with the step given as a number the host has done it
+    const double bc1 = a.step_dev ? -expm1((double)step * a.log_b1) : a.bc1;
+    const double bc2 = a.step_dev ? -expm1((double)step * a.log_b2) : a.bc2;
+    s_step_size = (float)(lr / bc1);
+    s_rbc2 = (float)(1.0 / sqrt(bc2));
     s_lr = (float)lr;
     s_skip = !(fabsf(gs) <= 3.402823466e38f) || step < 1;
     if (blockIdx.x == 0) {
@@ -287,174 +542,59 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Step
   }
   __syncthreads();
   if (s_skip) return;
-  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-  const float lr = s_lr, step_size = s_step_size, rbc2 = s_rbc2;
+  if (blockIdx.x == 0) {
+    for (int t = threadIdx.x; t < a.n; t += kThreads) {
+      if (!a.t[t].row_ids) continue;
+      const int64_t want = *a.t[t].n_rows;
+      if (want < 0 || want > a.t[t].max_rows) atomicCAS(a.status, HSTU_OK, HSTU_ERR_BAD_IDS);
+    }
+  }
+  StepConst k;
+  k.b1 = a.b1, k.omb1 = a.omb1, k.b2 = a.b2, k.omb2 = a.omb2, k.eps = a.eps;
+  k.gs = a.grad_scale ? *a.grad_scale : 1.f;
+  k.step_size = s_step_size, k.rbc2 = s_rbc2;
   const int64_t step = a.step_dev ? *a.step_dev : a.step;
-  int t = 0;
+  const uint64_t key0 = a.seed + (((uint64_t)step << 20) + (uint64_t)a.first + 1) * kGolden;
+  int t = -1;
+  int64_t rows = 0;
+  uint64_t key = 0;
   for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    while (t + 1 < a.n && c >= a.t[t + 1].chunk0) ++t;
+    if (t < 0 || (t + 1 < a.n && c >= a.t[t + 1].chunk0)) {
+      do ++t;
+      while (t + 1 < a.n && c >= a.t[t + 1].chunk0);
+      k.decay = s_lr * a.t[t].weight_decay;
+      key = split_mix(key0 + (uint64_t)t * kGolden);
+      if (a.t[t].row_ids)
+        rows = min(max(*a.t[t].n_rows, (int64_t)0), (int64_t)a.t[t].max_rows);
+    }
     const StepTensor& q = a.t[t];
     const int64_t b = (c - q.chunk0) * kChunkBlocks + warp;
-    int64_t g0, p0, block;  // first gradient and parameter element, block number in the tensor
-    int len;
+    BlockAt at;
     if (q.row_ids) {
-      const int64_t i = b / q.row_blocks;
+      const int64_t i = q.row_blocks == 1 ? b : (int64_t)((uint64_t)b / (uint32_t)q.row_blocks);
       const int j = (int)(b - i * q.row_blocks);
-      const int64_t want = *q.n_rows;
-      const int64_t rows = min(max(want, (int64_t)0), (int64_t)q.max_rows);
-      if (b == 0 && lane == 0 && want != rows) atomicCAS(a.status, HSTU_OK, HSTU_ERR_BAD_IDS);
       if (i >= rows) continue;
-      const int64_t row = q.row_ids[i];
-      const bool bad = row < 0 || row >= q.n / q.row_len || (i > 0 && q.row_ids[i - 1] >= row);
-      if (bad) {
+      const int64_t row = q.row_ids[i], before = i > 0 ? q.row_ids[i - 1] : -1;
+      if (row < 0 || row >= q.rows || before >= row) {
         if (lane == 0) atomicCAS(a.status, HSTU_OK, HSTU_ERR_BAD_IDS);
         continue;
       }
-      g0 = i * q.row_len + j * kBlockElems;
-      p0 = row * q.row_len + j * kBlockElems;
-      block = row * q.row_blocks + j;
-      len = min(kBlockElems, q.row_len - j * kBlockElems);
+      at.g0 = i * q.row_len + j * kBlockElems;
+      at.p0 = row * q.row_len + j * kBlockElems;
+      at.block = row * q.row_blocks + j;
+      at.len = min(kBlockElems, q.row_len - j * kBlockElems);
     } else {
-      g0 = p0 = b * kBlockElems;
-      if (g0 >= q.n) continue;
-      block = b;
-      len = (int)min((int64_t)kBlockElems, q.n - g0);
+      at.g0 = at.p0 = b * kBlockElems;
+      if (at.g0 >= q.n) continue;
+      at.block = b;
+      at.len = (int)min((int64_t)kBlockElems, q.n - at.g0);
     }
-    const bool whole = len == kBlockElems && !(q.row_ids && (q.row_len & 3));
-    const void* wide = q.master ? static_cast<const void*>(q.master) : q.param;
-    const int wide_dt = q.master ? HSTU_FP32 : q.param_dtype;
-    float g[2][4], p[2][4], m[2][4], v[2][4];
-    float ms = 0.f, vs = 0.f;
-    if (q.state8) {
-      ms = __uint_as_float((uint32_t)q.m_scale[block] << 23);
-      vs = __uint_as_float((uint32_t)q.v_scale[block] << 23);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int e = 4 * lane + 128 * j;
-      if (whole) {
-        load4(q.grad_dtype, q.grad, g0 + e, g[j]);
-        load4(wide_dt, wide, p0 + e, p[j]);
-        if (q.state8) {
-          const uint32_t mc = *reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(q.m) + p0 + e);
-          const uint32_t vc = *reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(q.v) + p0 + e);
-          const float2 m0 = e4m3x2_to_f32(mc & 0xffffu), m1 = e4m3x2_to_f32(mc >> 16);
-          const float2 v0 = e4m3x2_to_f32(vc & 0xffffu), v1 = e4m3x2_to_f32(vc >> 16);
-          m[j][0] = m0.x, m[j][1] = m0.y, m[j][2] = m1.x, m[j][3] = m1.y;
-          v[j][0] = v0.x, v[j][1] = v0.y, v[j][2] = v1.x, v[j][3] = v1.y;
-        } else {
-          load4(HSTU_FP32, q.m, p0 + e, m[j]);
-          load4(HSTU_FP32, q.v, p0 + e, v[j]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = e + i < len;
-          g[j][i] = in ? load_elem(q.grad_dtype, q.grad, g0 + e + i) : 0.f;
-          p[j][i] = in ? load_elem(wide_dt, wide, p0 + e + i) : 0.f;
-          if (q.state8) {
-            const uint32_t mc = in ? static_cast<uint8_t*>(q.m)[p0 + e + i] : 0;
-            const uint32_t vc = in ? static_cast<uint8_t*>(q.v)[p0 + e + i] : 0;
-            m[j][i] = e4m3x2_to_f32(mc).x;
-            v[j][i] = e4m3x2_to_f32(vc).x;
-          } else {
-            m[j][i] = in ? static_cast<float*>(q.m)[p0 + e + i] : 0.f;
-            v[j][i] = in ? static_cast<float*>(q.v)[p0 + e + i] : 0.f;
-          }
-        }
-      }
-    }
-    // The moments' products and sums are kept apart (no contraction), so that an 8-bit state
-    // does not depend on how the compiler fuses them.
-    const float decay = 1.f - lr * q.weight_decay;
-    float root[2][4], top_m = 0.f, top_r = 0.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (q.state8) {
-          m[j][i] = __fmul_rn(m[j][i], ms);
-          const float r = __fmul_rn(v[j][i], vs);
-          v[j][i] = __fmul_rn(r, r);
-        }
-        const float gg = __fmul_rn(g[j][i], gs);
-        m[j][i] = __fadd_rn(__fmul_rn(m[j][i], a.b1), __fmul_rn(gg, a.omb1));
-        v[j][i] = __fadd_rn(__fmul_rn(v[j][i], a.b2), __fmul_rn(__fmul_rn(gg, gg), a.omb2));
-        root[j][i] = __fsqrt_rn(v[j][i]);
-        const float u = __fdividef(m[j][i], root[j][i] * rbc2 + a.eps);
-        p[j][i] = p[j][i] * decay - u * step_size;
-        top_m = fmaxf(top_m, finite_abs(m[j][i]));
-        top_r = fmaxf(top_r, finite_abs(root[j][i]));
-      }
-    }
-    uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
-    if (q.state8) {
-      top_m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m)));
-      top_r = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top_r)));
-      const int mb = scale_byte(top_m), vb = scale_byte(top_r);
-      const float mi = __uint_as_float((uint32_t)(254 - mb) << 23);
-      const float vi = __uint_as_float((uint32_t)(254 - vb) << 23);
-      const uint64_t key = split_mix(
-          a.seed + ((((uint64_t)step << 20) + (uint64_t)(a.first + t)) + 1) * 0x9E3779B97F4A7C15ull);
-      const uint32_t base = mix32(mix32((uint32_t)block ^ (uint32_t)key) ^
-                                  (uint32_t)((uint64_t)block >> 32) ^ (uint32_t)(key >> 32));
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t r = mix32(base + (uint32_t)(4 * lane + 128 * j + i) * 0x9E3779B9u);
-          const uint32_t cm = e4m3_up(fabsf(m[j][i]) * mi, r & 0xffffu) |
-                              ((__float_as_uint(m[j][i]) >> 31) << 7);
-          const uint32_t cv = e4m3_up(root[j][i] * vi, r >> 16);
-          mc[j] |= cm << (8 * i);
-          vc[j] |= cv << (8 * i);
-        }
-      }
-      if (lane == 0) {
-        q.m_scale[block] = (uint8_t)mb;
-        q.v_scale[block] = (uint8_t)vb;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int e = 4 * lane + 128 * j;
-      if (whole) {
-        if (q.state8) {
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(q.m) + p0 + e) = mc[j];
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(q.v) + p0 + e) = vc[j];
-        } else {
-          store4(HSTU_FP32, q.m, p0 + e, m[j]);
-          store4(HSTU_FP32, q.v, p0 + e, v[j]);
-        }
-        if (q.master) store4(HSTU_FP32, q.master, p0 + e, p[j]);
-        store4(q.param_dtype, q.param, p0 + e, p[j]);
-        if (q.copy) {
-          float f[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            f[i] = fminf(fmaxf(rounded(q.param_dtype, p[j][i]), -65504.f), 65504.f);
-          store4(HSTU_FP16, q.copy, p0 + e, f);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (e + i >= len) continue;
-          const int64_t at = p0 + e + i;
-          if (q.state8) {
-            static_cast<uint8_t*>(q.m)[at] = (uint8_t)(mc[j] >> (8 * i));
-            static_cast<uint8_t*>(q.v)[at] = (uint8_t)(vc[j] >> (8 * i));
-          } else {
-            static_cast<float*>(q.m)[at] = m[j][i];
-            static_cast<float*>(q.v)[at] = v[j][i];
-          }
-          if (q.master) q.master[at] = p[j][i];
-          store_elem(q.param_dtype, q.param, at, p[j][i]);
-          if (q.copy)
-            q.copy[at] = __float2half_rn(
-                fminf(fmaxf(rounded(q.param_dtype, p[j][i]), -65504.f), 65504.f));
-        }
-      }
-    }
+    if ((at.len & 3) || (q.row_len & 3))
+      step_block_any(q, at, k, key);
+    else if (q.state8)
+      step_block<true>(q, at, k, key);
+    else
+      step_block<false>(q, at, k, key);
   }
 }
 
@@ -599,6 +739,8 @@ hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor
   a.eps = (float)h.eps;
   a.log_b1 = std::log(h.beta1);
   a.log_b2 = std::log(h.beta2);
+  a.bc1 = -std::expm1((double)h.step * a.log_b1);
+  a.bc2 = -std::expm1((double)h.step * a.log_b2);
   a.lr = h.lr;
   a.step = h.step;
   a.step_dev = h.step_dev;
@@ -626,6 +768,7 @@ hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor
       q.row_ids = t.row_ids;
       q.n_rows = t.n_rows;
       q.n = t.n;
+      q.rows = t.row_ids ? t.n / t.row_len : 0;
       q.row_len = t.row_ids ? (int32_t)t.row_len : 0;
       q.row_blocks = t.row_ids ? (int32_t)up_blocks(t.row_len) : 0;
       q.max_rows = (int32_t)t.max_rows;
