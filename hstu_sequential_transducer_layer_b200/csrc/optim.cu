@@ -2,8 +2,8 @@
 //
 // Both walk a list of tensors in one launch: the list is cut into blocks of
 // 256 consecutive elements (inside one tensor, and inside one row of a
-// row-sparse tensor), a warp per block, and chunks of 8 blocks are handed out
-// to a grid of resident thread blocks in turn.  The list's descriptors are
+// row-sparse tensor), a warp per block, and chunks of blocks are handed out to
+// a grid of resident thread blocks in turn.  The list's descriptors are
 // kernel parameters, so a step needs no copy to the device and can be
 // captured.
 #include <cuda_bf16.h>
@@ -19,8 +19,8 @@ namespace hstu {
 namespace {
 
 constexpr int kBlockElems = HSTU_STATE_BLOCK;
-constexpr int kChunkBlocks = 8;  // one per warp
-constexpr int kThreads = 32 * kChunkBlocks;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
 // Tensors of one launch: 120 bytes each, in 32,764 bytes of kernel parameters.
 constexpr int kMaxTensors = 256;
 
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(1024) k_norm_final(const NormFinal a) {
 struct StepTensor {
   const void* grad;
   void* param;
-  float* master;
+  void* master;
   __half* copy;
   void* m;
   void* v;
@@ -162,7 +162,9 @@ struct StepTensor {
   int32_t row_len, row_blocks, max_rows;
   int32_t chunk0;          // first chunk of this tensor
   float weight_decay;
-  uint8_t grad_dtype, param_dtype, state8;
+  uint8_t grad_dtype, param_dtype;
+  uint8_t per;             // consecutive blocks that a warp takes (<= 16)
+  uint8_t kind;            // 2 * (8-bit states) + (gradient and parameter read are fp32)
 };
 
 struct StepArgs {
@@ -201,12 +203,17 @@ DEVI uint64_t split_mix(uint64_t z) {
 // e4m3 code of the magnitude t (scaled, below 2^8), rounded up when the
 // 16-bit number r / 2^16 reaches the missing part: an e4m3 code step is 2^20
 // units of fp32's significand, so r * 16 is added and the rest cut.  Below
-// 2^-6 the codes have a fixed step, which adding 2^-6 gives them.  r20 is r
-// shifted left by 4, below 2^20.
-DEVI uint32_t e4m3_up(float t, uint32_t r20) {
+// 2^-6 the codes have a fixed step, which adding 2^-6 gives them.  Everything
+// is 4 bits further up, so that the code is the top byte and what is cut the
+// 24 bits below it; r8 is r shifted left by 8.
+DEVI uint32_t e4m3_up(float t, uint32_t r8) {
   const bool sub = t < 0.015625f;
   t = sub ? __fadd_rn(t, 0.015625f) : t;
-  return (__float_as_uint(t) + r20 - (sub ? 968u << 20 : 960u << 20)) >> 20;
+  return (__float_as_uint(t) << 4) + r8 - (sub ? 0xC8000000u : 0xC0000000u);
+}
+// Top bytes of four words.
+DEVI uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 DEVI float2 e4m3x2_to_f32(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
@@ -214,10 +221,23 @@ DEVI float2 e4m3x2_to_f32(uint32_t two) {
 }
 constexpr uint32_t kInfBits = 0x7f800000u;
 DEVI uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// The larger magnitude of the two, NaN if one is (its sign means nothing).
+DEVI float max_abs(float a, float b) {
+  float y;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// 1 / x to one ulp, x normal.
+DEVI float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Scale byte of a block whose largest finite magnitude has these bits:
 // 2^(byte - 127) puts it into [2^7, 2^8), half of e4m3's range, so rounding up
 // never saturates.
 DEVI int scale_byte(uint32_t top) { return max(1, (int)(top >> 23) - 7); }
+DEVI float scale_inverse(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 
 // Four consecutive elements as they lie in memory (16-bit types: x and y).
 DEVI uint4 raw4(bool wide, const uint8_t* p, int e) {
@@ -240,13 +260,17 @@ DEVI void widen4(int dtype, const uint4& r, float (&f)[4]) {
 }
 DEVI uint32_t bits2(const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); }
 DEVI uint32_t bits2(const __half2& x) { return *reinterpret_cast<const uint32_t*>(&x); }
+// fp16 pair, saturating at +-65504 as hstu_bf16_to_f16 does.
+DEVI uint32_t half2_sat(float2 x) {
+  return bits2(__hmin2(__hmax2(__floats2half2_rn(x.x, x.y), __float2half2_rn(-65504.f)),
+                       __float2half2_rn(65504.f)));
+}
 // What storing x in `dtype` leaves of it.
 DEVI float rounded(int dtype, float x) {
   return dtype == HSTU_FP32   ? x
          : dtype == HSTU_BF16 ? __bfloat162float(__float2bfloat16_rn(x))
                               : __half2float(__float2half_rn(x));
 }
-DEVI __half half_sat(float x) { return __float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)); }
 DEVI void store_elem(int dtype, void* p, int64_t i, float x) {
   if (dtype == HSTU_FP32)
     static_cast<float*>(p)[i] = x;
@@ -261,45 +285,27 @@ struct StepConst {
   float b1, omb1, b2, omb2, eps, gs, step_size, rbc2, decay;
 };
 
-// One element: m, v and p after the step, root = sqrt(v).  The moments'
-// products and sums are kept apart (no contraction), so that an 8-bit state
-// does not depend on how the compiler fuses them.
-DEVI void step_elem(const StepConst& k, float g, float& m, float& v, float& p, float& root) {
+// m and v after the step.  Products and sums are kept apart (no contraction),
+// so that an 8-bit state does not depend on how the compiler fuses them.
+DEVI void moments(const StepConst& k, float g, float& m, float& v) {
   g = __fmul_rn(g, k.gs);
   m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.omb1));
   v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.omb2));
-  root = __fsqrt_rn(v);
-  const float u = __fdividef(m, fmaf(root, k.rbc2, k.eps));
-  p -= fmaf(p, k.decay, u * k.step_size);
+}
+// The new parameter; eps >= 2^-126, so the denominator is a normal number.
+DEVI float new_param(const StepConst& k, float p, float m, float root) {
+  return p - fmaf(p, k.decay, m * rcp_approx(fmaf(root, k.rbc2, k.eps)) * k.step_size);
 }
 
-// Key of a block's random numbers.
+// Key of a block's random numbers, and an element's 32 random bits: the low
+// half is m's number, the high half r's.
 DEVI uint32_t block_key(uint64_t key, int64_t block) {
   return mix32(mix32((uint32_t)block ^ (uint32_t)key) ^ (uint32_t)((uint64_t)block >> 32) ^
                (uint32_t)(key >> 32));
 }
 DEVI uint32_t elem_random(uint32_t base, int e) { return mix32(base + (uint32_t)e * 0x9E3779B9u); }
-
-// Four codes of each state, element e0 the first.  CHECK: some value is not
-// finite; those become NaN.
-template <bool CHECK>
-DEVI void encode4(const float (&m)[4], const float (&root)[4], float mi, float vi, uint32_t base,
-                  int e0, uint32_t& mc, uint32_t& vc) {
-  mc = vc = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t r = elem_random(base, e0 + i);
-    uint32_t a = e4m3_up(fabsf(m[i]) * mi, (r << 4) & 0xffff0u);
-    uint32_t b = e4m3_up(root[i] * vi, (r >> 12) & 0xffff0u);
-    if (CHECK) {
-      a = abs_bits(m[i]) < kInfBits ? a : 0x7fu;
-      b = abs_bits(root[i]) < kInfBits ? b : 0x7fu;
-    }
-    a |= (__float_as_uint(m[i]) >> 24) & 0x80u;
-    mc |= a << (8 * i);
-    vc |= b << (8 * i);
-  }
-}
+DEVI uint32_t low16_up(uint32_t r) { return __byte_perm(r, 0, 0x4104); }   // << 8
+DEVI uint32_t high16_up(uint32_t r) { return __byte_perm(r, 0, 0x4324); }
 
 // Where a block of up to 256 elements lies.
 struct BlockAt {
@@ -307,60 +313,91 @@ struct BlockAt {
   int len;
 };
 
+// Where a tensor's elements are read: FAST tensors (the gradient and the
+// parameter that is read -- the master, or the parameter itself -- are fp32,
+// as this library's backward pass and trainer have them) need no type asked
+// for in the loop.
+template <bool FAST>
+DEVI bool grad_wide(const StepTensor& q) { return FAST || q.grad_dtype == HSTU_FP32; }
+template <bool FAST>
+DEVI bool param_wide(const StepTensor& q) {
+  return FAST || q.master || q.param_dtype == HSTU_FP32;
+}
+
+// Stores four new parameters and what is kept of them.
+template <bool FAST>
+DEVI void store_param(const StepTensor& q, int64_t at, const float (&p)[4]) {
+  if (param_wide<FAST>(q))
+    *reinterpret_cast<float4*>(static_cast<float*>(q.master ? q.master : q.param) + at) =
+        make_float4(p[0], p[1], p[2], p[3]);
+  float2 x = make_float2(p[0], p[1]), y = make_float2(p[2], p[3]);  // as stored
+  if (q.param_dtype == HSTU_BF16) {
+    const __nv_bfloat162 s = __floats2bfloat162_rn(x.x, x.y), t = __floats2bfloat162_rn(y.x, y.y);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(q.param) + at) =
+        make_uint2(bits2(s), bits2(t));
+    x = __bfloat1622float2(s), y = __bfloat1622float2(t);
+  } else if (q.param_dtype == HSTU_FP16) {
+    const __half2 s = __floats2half2_rn(x.x, x.y), t = __floats2half2_rn(y.x, y.y);
+    *reinterpret_cast<uint2*>(static_cast<__half*>(q.param) + at) = make_uint2(bits2(s), bits2(t));
+    x = __half22float2(s), y = __half22float2(t);
+  }
+  if (q.copy) *reinterpret_cast<uint2*>(q.copy + at) = make_uint2(half2_sat(x), half2_sat(y));
+}
+
 // The step of one block whose length is a multiple of 4 and whose rows are
-// 16-byte aligned.  Lane l holds elements 4 l + 128 j + (0..3), j = 0, 1, so
-// every access of a warp is to consecutive addresses; all of a lane's loads
-// are issued before the first one is used.
-template <bool S8>
-DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k, uint64_t key) {
+// 16-byte aligned.  WHOLE: 256 elements.  Lane l holds elements 4 l + 128 j +
+// (0..3), j = 0, 1, so every access of a warp is to consecutive addresses;
+// all of a lane's loads are issued before the first one is used.  8-bit
+// states: the block's scale bytes are `bytes` of lanes u (m) and 16 + u (v), and
+// are replaced by the new ones.
+template <bool S8, bool FAST, bool WHOLE>
+DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k, uint64_t key,
+                     int u, int& bytes) {
   const int lane = threadIdx.x & 31;
-  const bool gw = q.grad_dtype == HSTU_FP32;
-  const bool pw = q.master || q.param_dtype == HSTU_FP32;
+  const bool gw = grad_wide<FAST>(q), pw = param_wide<FAST>(q);
   const uint8_t* gp = static_cast<const uint8_t*>(q.grad) + (at.g0 << (gw ? 2 : 1));
-  uint8_t* wp = q.master ? reinterpret_cast<uint8_t*>(q.master + at.p0)
-                         : static_cast<uint8_t*>(q.param) + (at.p0 << (pw ? 2 : 1));
+  const uint8_t* wp = static_cast<const uint8_t*>(q.master ? q.master : q.param) +
+                      (at.p0 << (pw ? 2 : 1));
   uint8_t* mp = static_cast<uint8_t*>(q.m) + (S8 ? at.p0 : 4 * at.p0);
   uint8_t* vp = static_cast<uint8_t*>(q.v) + (S8 ? at.p0 : 4 * at.p0);
-  uint4 gr[2], pr[2];
-  float m[2][4], v[2][4], p[2][4], root[2][4];
-  uint32_t mc[2], vc[2];
-  float ms = 0.f, vs = 0.f;
-  bool in[2];
+  uint4 gr[2], pr[2], mr[2], vr[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int e = 4 * lane + 128 * j;
-    in[j] = e < at.len;
-    gr[j] = pr[j] = make_uint4(0, 0, 0, 0);
-    mc[j] = vc[j] = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m[j][i] = v[j][i] = 0.f;
-    if (in[j]) {
-      gr[j] = raw4(gw, gp, e);
-      pr[j] = raw4(pw, wp, e);
-      if (S8) {
-        mc[j] = *reinterpret_cast<const uint32_t*>(mp + e);
-        vc[j] = *reinterpret_cast<const uint32_t*>(vp + e);
-      } else {
-        widen4(HSTU_FP32, raw4(true, mp, e), m[j]);
-        widen4(HSTU_FP32, raw4(true, vp, e), v[j]);
-      }
+    if (!WHOLE && e >= at.len) {
+      gr[j] = pr[j] = mr[j] = vr[j] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    gr[j] = raw4(gw, gp, e);
+    pr[j] = raw4(pw, wp, e);
+    if (S8) {
+      mr[j].x = *reinterpret_cast<const uint32_t*>(mp + e);
+      vr[j].x = *reinterpret_cast<const uint32_t*>(vp + e);
+    } else {
+      mr[j] = raw4(true, mp, e);
+      vr[j] = raw4(true, vp, e);
     }
   }
+  float ms = 0.f, vs = 0.f;
   if (S8) {
-    ms = __uint_as_float((uint32_t)q.m_scale[at.block] << 23);
-    vs = __uint_as_float((uint32_t)q.v_scale[at.block] << 23);
+    ms = __uint_as_float((uint32_t)__shfl_sync(0xffffffffu, bytes, u) << 23);
+    vs = __uint_as_float((uint32_t)__shfl_sync(0xffffffffu, bytes, 16 + u) << 23);
   }
-  uint32_t top_m = 0, top_r = 0;
+  float m[2][4], v[2][4], top_m = 0.f, top_r = 0.f;  // 8-bit states: v becomes the root
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    float g[4];
-    widen4(q.grad_dtype, gr[j], g);
-    widen4(pw ? HSTU_FP32 : q.param_dtype, pr[j], p[j]);
+    const int e = 4 * lane + 128 * j;
+    float g[4], p[4];
+    widen4(FAST ? HSTU_FP32 : q.grad_dtype, gr[j], g);
+    widen4(pw ? HSTU_FP32 : q.param_dtype, pr[j], p);
     if (S8) {
-      const float2 m0 = e4m3x2_to_f32(mc[j] & 0xffffu), m1 = e4m3x2_to_f32(mc[j] >> 16);
-      const float2 v0 = e4m3x2_to_f32(vc[j] & 0xffffu), v1 = e4m3x2_to_f32(vc[j] >> 16);
+      const float2 m0 = e4m3x2_to_f32(mr[j].x & 0xffffu), m1 = e4m3x2_to_f32(mr[j].x >> 16);
+      const float2 v0 = e4m3x2_to_f32(vr[j].x & 0xffffu), v1 = e4m3x2_to_f32(vr[j].x >> 16);
       m[j][0] = m0.x, m[j][1] = m0.y, m[j][2] = m1.x, m[j][3] = m1.y;
       v[j][0] = v0.x, v[j][1] = v0.y, v[j][2] = v1.x, v[j][3] = v1.y;
+    } else {
+      widen4(HSTU_FP32, mr[j], m[j]);
+      widen4(HSTU_FP32, vr[j], v[j]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -369,97 +406,79 @@ DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k,
         v[j][i] = __fmul_rn(v[j][i], vs);
         v[j][i] = __fmul_rn(v[j][i], v[j][i]);
       }
-      step_elem(k, g[i], m[j][i], v[j][i], p[j][i], root[j][i]);
+      moments(k, g[i], m[j][i], v[j][i]);
+      const float root = __fsqrt_rn(v[j][i]);
+      p[i] = new_param(k, p[i], m[j][i], root);
       if (S8) {
-        top_m = max(top_m, abs_bits(m[j][i]));
-        top_r = max(top_r, abs_bits(root[j][i]));
+        v[j][i] = root;
+        top_m = max_abs(top_m, m[j][i]);
+        top_r = max_abs(top_r, root);
       }
     }
-  }
-  if (S8) {
-    top_m = __reduce_max_sync(0xffffffffu, top_m);
-    top_r = __reduce_max_sync(0xffffffffu, top_r);
-    const bool odd = top_m >= kInfBits || top_r >= kInfBits;  // the same for the whole warp
-    if (odd) {
-      top_m = top_r = 0;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a = abs_bits(m[j][i]), b = abs_bits(root[j][i]);
-          top_m = max(top_m, a < kInfBits ? a : 0);
-          top_r = max(top_r, b < kInfBits ? b : 0);
-        }
-      }
-      top_m = __reduce_max_sync(0xffffffffu, top_m);
-      top_r = __reduce_max_sync(0xffffffffu, top_r);
-    }
-    const int mb = scale_byte(top_m), vb = scale_byte(top_r);
-    const float mi = __uint_as_float((uint32_t)(254 - mb) << 23);
-    const float vi = __uint_as_float((uint32_t)(254 - vb) << 23);
-    const uint32_t base = block_key(key, at.block);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (odd)
-        encode4<true>(m[j], root[j], mi, vi, base, 4 * lane + 128 * j, mc[j], vc[j]);
-      else
-        encode4<false>(m[j], root[j], mi, vi, base, 4 * lane + 128 * j, mc[j], vc[j]);
-    }
-    if (lane == 0) {
-      q.m_scale[at.block] = (uint8_t)mb;
-      q.v_scale[at.block] = (uint8_t)vb;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (!in[j]) continue;
-    const int e = 4 * lane + 128 * j;
-    if (S8) {
-      *reinterpret_cast<uint32_t*>(mp + e) = mc[j];
-      *reinterpret_cast<uint32_t*>(vp + e) = vc[j];
-    } else {
+    if (!WHOLE && e >= at.len) continue;
+    if (!S8) {
       *reinterpret_cast<float4*>(mp + 4 * e) = make_float4(m[j][0], m[j][1], m[j][2], m[j][3]);
       *reinterpret_cast<float4*>(vp + 4 * e) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
     }
-    if (pw) *reinterpret_cast<float4*>(wp + 4 * e) = make_float4(p[j][0], p[j][1], p[j][2], p[j][3]);
-    __half2 h0, h1;  // the fp16 copy, of the stored value
-    if (q.param_dtype == HSTU_BF16) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(p[j][0], p[j][1]);
-      const __nv_bfloat162 y = __floats2bfloat162_rn(p[j][2], p[j][3]);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(q.param) + at.p0 + e) =
-          make_uint2(bits2(x), bits2(y));
-      if (q.copy) {
-        const float2 a = __bfloat1622float2(x), b = __bfloat1622float2(y);
-        h0 = __halves2half2(half_sat(a.x), half_sat(a.y));
-        h1 = __halves2half2(half_sat(b.x), half_sat(b.y));
+    store_param<FAST>(q, at.p0 + e, p);
+  }
+  if (!S8) return;
+  uint32_t tm = __reduce_max_sync(0xffffffffu, abs_bits(top_m));
+  uint32_t tr = __reduce_max_sync(0xffffffffu, abs_bits(top_r));
+  uint32_t m_nan[2] = {0, 0}, v_nan[2] = {0, 0};  // codes of what is not finite
+  if (tm >= kInfBits || tr >= kInfBits) {          // the same for the whole warp; rare
+    tm = tr = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (abs_bits(m[j][i]) >= kInfBits) {
+          m_nan[j] |= (0x7fu | ((__float_as_uint(m[j][i]) >> 24) & 0x80u)) << (8 * i);
+          m[j][i] = 0.f;
+        }
+        if (abs_bits(v[j][i]) >= kInfBits) {
+          v_nan[j] |= 0x7fu << (8 * i);
+          v[j][i] = 0.f;
+        }
+        tm = max(tm, abs_bits(m[j][i]));
+        tr = max(tr, abs_bits(v[j][i]));
       }
-    } else if (q.param_dtype == HSTU_FP16) {
-      const __half2 x = __floats2half2_rn(p[j][0], p[j][1]);
-      const __half2 y = __floats2half2_rn(p[j][2], p[j][3]);
-      *reinterpret_cast<uint2*>(static_cast<__half*>(q.param) + at.p0 + e) =
-          make_uint2(bits2(x), bits2(y));
-      if (q.copy) {
-        const float2 a = __half22float2(x), b = __half22float2(y);
-        h0 = __halves2half2(half_sat(a.x), half_sat(a.y));
-        h1 = __halves2half2(half_sat(b.x), half_sat(b.y));
-      }
-    } else if (q.copy) {
-      h0 = __halves2half2(half_sat(p[j][0]), half_sat(p[j][1]));
-      h1 = __halves2half2(half_sat(p[j][2]), half_sat(p[j][3]));
     }
-    if (q.copy)
-      *reinterpret_cast<uint2*>(q.copy + at.p0 + e) = make_uint2(bits2(h0), bits2(h1));
+    tm = __reduce_max_sync(0xffffffffu, tm);
+    tr = __reduce_max_sync(0xffffffffu, tr);
+  }
+  const int m_byte = scale_byte(tm), v_byte = scale_byte(tr);
+  if ((lane & 15) == u) bytes = lane < 16 ? m_byte : v_byte;
+  const float mi = scale_inverse(m_byte), vi = scale_inverse(v_byte);
+  const uint32_t base = block_key(key, at.block) + (uint32_t)(4 * lane) * 0x9E3779B9u;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = 4 * lane + 128 * j;
+    if (!WHOLE && e >= at.len) continue;
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t r = elem_random(base, 128 * j + i);
+      a[i] = e4m3_up(fabsf(m[j][i]) * mi, low16_up(r));
+      b[i] = e4m3_up(v[j][i] * vi, high16_up(r));
+    }
+    const uint32_t sign = top_bytes(__float_as_uint(m[j][0]), __float_as_uint(m[j][1]),
+                                    __float_as_uint(m[j][2]), __float_as_uint(m[j][3]));
+    *reinterpret_cast<uint32_t*>(mp + e) =
+        top_bytes(a[0], a[1], a[2], a[3]) | (sign & 0x80808080u) | m_nan[j];
+    *reinterpret_cast<uint32_t*>(vp + e) = top_bytes(b[0], b[1], b[2], b[3]) | v_nan[j];
   }
 }
 
-// The same for any other block (the end of a tensor, rows that are not
-// multiples of 4 elements), element by element: lane l takes elements l + 32 i.
+// The same for any block (the end of a tensor, rows that are not multiples of
+// 4 elements), element by element: lane l takes elements l + 32 i.
+template <bool S8>
 DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst& k, uint64_t key) {
   const int lane = threadIdx.x & 31;
-  const void* wide = q.master ? static_cast<const void*>(q.master) : q.param;
+  const void* wide = q.master ? q.master : q.param;
   const int wide_dt = q.master ? HSTU_FP32 : q.param_dtype;
   float ms = 0.f, vs = 0.f, m[8], root[8];
-  if (q.state8) {
+  if (S8) {
     ms = __uint_as_float((uint32_t)q.m_scale[at.block] << 23);
     vs = __uint_as_float((uint32_t)q.v_scale[at.block] << 23);
   }
@@ -472,7 +491,7 @@ DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst
     const int64_t x = at.p0 + e;
     float v, p = load_elem(wide_dt, wide, x);
     const float g = load_elem(q.grad_dtype, q.grad, at.g0 + e);
-    if (q.state8) {
+    if (S8) {
       m[i] = __fmul_rn(e4m3x2_to_f32(static_cast<uint8_t*>(q.m)[x]).x, ms);
       v = __fmul_rn(e4m3x2_to_f32(static_cast<uint8_t*>(q.v)[x]).x, vs);
       v = __fmul_rn(v, v);
@@ -480,32 +499,36 @@ DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst
       m[i] = static_cast<float*>(q.m)[x];
       v = static_cast<float*>(q.v)[x];
     }
-    step_elem(k, g, m[i], v, p, root[i]);
-    if (!q.state8) {
+    moments(k, g, m[i], v);
+    root[i] = __fsqrt_rn(v);
+    p = new_param(k, p, m[i], root[i]);
+    if (!S8) {
       static_cast<float*>(q.m)[x] = m[i];
       static_cast<float*>(q.v)[x] = v;
     }
-    if (q.master) q.master[x] = p;
+    if (q.master) static_cast<float*>(q.master)[x] = p;
     store_elem(q.param_dtype, q.param, x, p);
-    if (q.copy) q.copy[x] = half_sat(rounded(q.param_dtype, p));
+    if (q.copy) {
+      const float y = rounded(q.param_dtype, p);
+      q.copy[x] = __ushort_as_half((unsigned short)half2_sat(make_float2(y, y)));
+    }
     const uint32_t a = abs_bits(m[i]), b = abs_bits(root[i]);
     top_m = max(top_m, a < kInfBits ? a : 0);
     top_r = max(top_r, b < kInfBits ? b : 0);
   }
-  if (!q.state8) return;
+  if (!S8) return;
   const int mb = scale_byte(__reduce_max_sync(0xffffffffu, top_m));
   const int vb = scale_byte(__reduce_max_sync(0xffffffffu, top_r));
-  const float mi = __uint_as_float((uint32_t)(254 - mb) << 23);
-  const float vi = __uint_as_float((uint32_t)(254 - vb) << 23);
+  const float mi = scale_inverse(mb), vi = scale_inverse(vb);
   const uint32_t base = block_key(key, at.block);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int e = lane + 32 * i;
     if (e >= at.len) continue;
     const uint32_t r = elem_random(base, e);
-    const uint32_t a = abs_bits(m[i]) < kInfBits ? e4m3_up(fabsf(m[i]) * mi, (r << 4) & 0xffff0u)
+    const uint32_t a = abs_bits(m[i]) < kInfBits ? e4m3_up(fabsf(m[i]) * mi, low16_up(r)) >> 24
                                                  : 0x7fu;
-    const uint32_t b = abs_bits(root[i]) < kInfBits ? e4m3_up(root[i] * vi, (r >> 12) & 0xffff0u)
+    const uint32_t b = abs_bits(root[i]) < kInfBits ? e4m3_up(root[i] * vi, high16_up(r)) >> 24
                                                     : 0x7fu;
     static_cast<uint8_t*>(q.m)[at.p0 + e] =
         (uint8_t)(a | ((__float_as_uint(m[i]) >> 24) & 0x80u));
@@ -517,13 +540,45 @@ DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst
   }
 }
 
-// One step of every tensor, a warp per block of 256 elements.
-// Bandwidth-bound: per element the gradient, the states and the (master)
-// parameter are read once and the results written once.
-__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ StepArgs a) {
-  __shared__ float s_lr, s_step_size, s_rbc2;
+// Block b of a row-sparse tensor; false (and the status set) if its row is not
+// one of the table or not above the row before.
+DEVI bool row_block(const StepTensor& q, int64_t b, int* status, BlockAt& at) {
+  const int64_t i = q.row_blocks == 1 ? b : (int64_t)((uint64_t)b / (uint32_t)q.row_blocks);
+  const int j = (int)(b - i * q.row_blocks);
+  const int64_t row = q.row_ids[i], before = i > 0 ? q.row_ids[i - 1] : -1;
+  if (row < 0 || row >= q.rows || before >= row) {
+    if ((threadIdx.x & 31) == 0) atomicCAS(status, HSTU_OK, HSTU_ERR_BAD_IDS);
+    return false;
+  }
+  at.g0 = i * q.row_len + j * kBlockElems;
+  at.p0 = row * q.row_len + j * kBlockElems;
+  at.block = row * q.row_blocks + j;
+  at.len = min(kBlockElems, q.row_len - j * kBlockElems);
+  return true;
+}
+
+// One step of every tensor of the list whose states have this width and whose
+// types are FAST or not, a warp per block of 256 elements.  Bandwidth-bound:
+// per element the gradient, the states and the (master) parameter are read
+// once and the results written once.
+//
+// 8-bit states: a warp takes 8 consecutive blocks of a large dense tensor at a
+// time and reads and writes their scale bytes together.  One block at a time,
+// the bytes of a 32-byte sector were read and written by 32 warps on several
+// SMs, which cost 20 to 45 us of 184 on 42M parameters.
+//
+// Thread blocks of 128 threads per SM, measured on 42M parameters: fp32 states
+// 6 resident (80 registers), 16 launched (218 us; 8 resident at 64 registers
+// 235, 16 resident waves of one launch 236: the hardware's handing out of
+// thread blocks evens out what a fixed share does not); 8-bit states, bound by
+// instructions as much as by memory, 7 resident and launched (160 us; 8
+// resident at 64 registers, which spill, 171; 6 164).
+template <bool S8, bool FAST>
+__global__ void __launch_bounds__(kThreads, S8 ? 7 : 6)
+    k_adamw(const __grid_constant__ StepArgs a) {
+  __shared__ StepConst s_k;
+  __shared__ float s_lr;
   __shared__ int s_skip;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     const int64_t step = a.step_dev ? *a.step_dev : a.step;
     const float gs = a.grad_scale ? *a.grad_scale : 1.f;
@@ -531,8 +586,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ S
     // 1 - b^t without cancellation; with the step given as a number the host has done it
     const double bc1 = a.step_dev ? -expm1((double)step * a.log_b1) : a.bc1;
     const double bc2 = a.step_dev ? -expm1((double)step * a.log_b2) : a.bc2;
-    s_step_size = (float)(lr / bc1);
-    s_rbc2 = (float)(1.0 / sqrt(bc2));
+    s_k.b1 = a.b1, s_k.omb1 = a.omb1, s_k.b2 = a.b2, s_k.omb2 = a.omb2, s_k.eps = a.eps;
+    s_k.gs = gs;
+    s_k.step_size = (float)(lr / bc1);
+    s_k.rbc2 = (float)(1.0 / sqrt(bc2));
+    s_k.decay = 0.f;
     s_lr = (float)lr;
     s_skip = !(fabsf(gs) <= 3.402823466e38f) || step < 1;
     if (blockIdx.x == 0) {
@@ -549,52 +607,63 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ S
       if (want < 0 || want > a.t[t].max_rows) atomicCAS(a.status, HSTU_OK, HSTU_ERR_BAD_IDS);
     }
   }
-  StepConst k;
-  k.b1 = a.b1, k.omb1 = a.omb1, k.b2 = a.b2, k.omb2 = a.omb2, k.eps = a.eps;
-  k.gs = a.grad_scale ? *a.grad_scale : 1.f;
-  k.step_size = s_step_size, k.rbc2 = s_rbc2;
+  StepConst k = s_k;
   const int64_t step = a.step_dev ? *a.step_dev : a.step;
   const uint64_t key0 = a.seed + (((uint64_t)step << 20) + (uint64_t)a.first + 1) * kGolden;
-  int t = -1;
-  int64_t rows = 0;
-  uint64_t key = 0;
-  for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    if (t < 0 || (t + 1 < a.n && c >= a.t[t + 1].chunk0)) {
-      do ++t;
-      while (t + 1 < a.n && c >= a.t[t + 1].chunk0);
-      k.decay = s_lr * a.t[t].weight_decay;
-      key = split_mix(key0 + (uint64_t)t * kGolden);
-      if (a.t[t].row_ids)
-        rows = min(max(*a.t[t].n_rows, (int64_t)0), (int64_t)a.t[t].max_rows);
-    }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t c = blockIdx.x;  // this thread block's next chunk of the list
+  for (int t = 0; t < a.n; ++t) {
     const StepTensor& q = a.t[t];
-    const int64_t b = (c - q.chunk0) * kChunkBlocks + warp;
+    const int64_t end = t + 1 < a.n ? a.t[t + 1].chunk0 : a.chunks;
+    if (c >= end) continue;
+    const int per = q.per;
+    int64_t b = ((c - q.chunk0) * kWarps + warp) * per;
+    const int64_t next = (int64_t)gridDim.x * kWarps * per;
+    c += (end - c + gridDim.x - 1) / gridDim.x * gridDim.x;
+    if (q.kind != 2 * S8 + FAST) continue;
+    k.decay = s_lr * q.weight_decay;
+    const uint64_t key = split_mix(key0 + (uint64_t)t * kGolden);
     BlockAt at;
-    if (q.row_ids) {
-      const int64_t i = q.row_blocks == 1 ? b : (int64_t)((uint64_t)b / (uint32_t)q.row_blocks);
-      const int j = (int)(b - i * q.row_blocks);
-      if (i >= rows) continue;
-      const int64_t row = q.row_ids[i], before = i > 0 ? q.row_ids[i - 1] : -1;
-      if (row < 0 || row >= q.rows || before >= row) {
-        if (lane == 0) atomicCAS(a.status, HSTU_OK, HSTU_ERR_BAD_IDS);
-        continue;
+    if (!q.row_ids) {
+      const int64_t whole = q.n / kBlockElems;
+      for (; b < whole; b += next) {
+        const int n = (int)min((int64_t)per, whole - b);
+        // lane u: the scale byte of m of block b + u, lane 16 + u: of v
+        uint8_t* scale = lane < 16 ? q.m_scale : q.v_scale;
+        int bytes = 0;
+        if (S8 && (lane & 15) < n) bytes = scale[b + (lane & 15)];
+        at.len = kBlockElems;
+        for (int u = 0; u < n; ++u) {
+          at.block = b + u;
+          at.g0 = at.p0 = at.block * kBlockElems;
+          step_block<S8, FAST, true>(q, at, k, key, u, bytes);
+        }
+        if (S8 && (lane & 15) < n) scale[b + (lane & 15)] = (uint8_t)bytes;
+        if (b + n == whole) break;
       }
-      at.g0 = i * q.row_len + j * kBlockElems;
-      at.p0 = row * q.row_len + j * kBlockElems;
-      at.block = row * q.row_blocks + j;
-      at.len = min(kBlockElems, q.row_len - j * kBlockElems);
+      // the shorter block behind the last whole one is with the warp whose turn it is
+      at.len = (int)(q.n - whole * kBlockElems);
+      if (at.len && whole / per == b / per) {
+        at.block = whole;
+        at.g0 = at.p0 = whole * kBlockElems;
+        step_block_any<S8>(q, at, k, key);
+      }
     } else {
-      at.g0 = at.p0 = b * kBlockElems;
-      if (at.g0 >= q.n) continue;
-      at.block = b;
-      at.len = (int)min((int64_t)kBlockElems, q.n - at.g0);
+      const int64_t blocks =
+          min(max(*q.n_rows, (int64_t)0), (int64_t)q.max_rows) * q.row_blocks;
+      if (q.row_len % 4) {
+        for (; b < blocks; b += next)
+          if (row_block(q, b, a.status, at)) step_block_any<S8>(q, at, k, key);
+      } else {
+        for (; b < blocks; b += next) {
+          if (!row_block(q, b, a.status, at)) continue;
+          uint8_t* scale = lane < 16 ? q.m_scale : q.v_scale;
+          int bytes = S8 ? scale[at.block] : 0;
+          step_block<S8, FAST, false>(q, at, k, key, 0, bytes);
+          if (S8 && (lane & 15) == 0) scale[at.block] = (uint8_t)bytes;
+        }
+      }
     }
-    if ((at.len & 3) || (q.row_len & 3))
-      step_block_any(q, at, k, key);
-    else if (q.state8)
-      step_block<true>(q, at, k, key);
-    else
-      step_block<false>(q, at, k, key);
   }
 }
 
@@ -609,6 +678,7 @@ hstu_status cuda_status(cudaError_t e, const char* where) {
   return HSTU_ERR_CUDA;
 }
 
+constexpr int kPerWarp = 8;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
 // The gradient's part of a descriptor; *sparse: only some rows have one.
@@ -704,8 +774,8 @@ hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor
   if (!args || n_tensors < 0 || (n_tensors > 0 && !tensors)) return HSTU_ERR_INVALID_ARG;
   if (n_tensors > HSTU_MAX_TENSORS) return HSTU_ERR_UNSUPPORTED;
   const hstu_adamw_args& h = *args;
-  if (!(h.beta1 >= 0 && h.beta1 < 1) || !(h.beta2 >= 0 && h.beta2 < 1) || !(h.eps > 0) ||
-      !std::isfinite(h.eps) || !std::isfinite(h.lr) || (!h.step_dev && h.step < 1))
+  if (!(h.beta1 >= 0 && h.beta1 < 1) || !(h.beta2 >= 0 && h.beta2 < 1) || !(h.eps >= 1.17549435e-38) ||
+      !(h.eps <= 3.402823466e38) || !std::isfinite(h.lr) || (!h.step_dev && h.step < 1))
     return HSTU_ERR_INVALID_ARG;
   bool fails = h.step_dev != nullptr;
   int64_t blocks = 0;
@@ -723,9 +793,9 @@ hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor
     if (t.n > 0 && (!t.param || !t.m || !t.v)) return HSTU_ERR_INVALID_ARG;
     if (t.n > 0 && t.state_bits == 8 && (!t.m_scale || !t.v_scale)) return HSTU_ERR_INVALID_ARG;
     fails |= sparse;
-    blocks += tensor_blocks(t) + kChunkBlocks;
+    blocks += tensor_blocks(t) + kWarps;
   }
-  if (blocks / kChunkBlocks > 0x7fffffffll) return HSTU_ERR_UNSUPPORTED;
+  if (blocks / kWarps > 0x7fffffffll) return HSTU_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < hstu_adamw_workspace_size() || !al256(ws)) return HSTU_ERR_WORKSPACE;
   if (fails) {
     const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), s);
@@ -749,6 +819,8 @@ hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor
   a.seed = h.seed;
   a.status = static_cast<int*>(ws);
   a.set_ok = !fails;
+  // one block at a time where more would leave warps without work
+  const bool large = blocks >= (int64_t)num_sms() * 32 * kPerWarp * 2;
   int i = 0;
   do {
     a.first = i;
@@ -776,14 +848,26 @@ hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor
       q.weight_decay = (float)t.weight_decay;
       q.grad_dtype = (uint8_t)t.grad_dtype;
       q.param_dtype = (uint8_t)t.param_dtype;
-      q.state8 = t.state_bits == 8;
-      a.chunks += (tensor_blocks(t) + kChunkBlocks - 1) / kChunkBlocks;
+      q.kind = (uint8_t)(2 * (t.state_bits == 8) +
+                         (t.grad_dtype == HSTU_FP32 && (q.master || t.param_dtype == HSTU_FP32)));
+      q.per = large && t.state_bits == 8 && !t.row_ids ? kPerWarp : 1;
+      const int64_t chunk = kWarps * q.per;
+      a.chunks += (tensor_blocks(t) + chunk - 1) / chunk;
     }
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(a.chunks, num_sms() * 8));
-    LaunchScope ls(K_ADAMW, s);
-    k_adamw<<<grid, kThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");
+    // a kernel per kind of tensor: one list seldom has more than one or two
+    unsigned kinds = a.n == 0 ? 1u : 0u;
+    for (int j = 0; j < a.n; ++j) kinds |= 1u << a.t[j].kind;
+    static void (*const fn[4])(StepArgs) = {k_adamw<false, false>, k_adamw<false, true>,
+                                            k_adamw<true, false>, k_adamw<true, true>};
+    for (int j = 0; j < 4; ++j) {
+      if (!(kinds >> j & 1)) continue;
+      LaunchScope ls(K_ADAMW, s);
+      const int grid = (int)std::max<int64_t>(
+          1, std::min<int64_t>(a.chunks, num_sms() * (j >= 2 ? 7 : 16)));
+      fn[j]<<<grid, kThreads, 0, s>>>(a);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");
+    }
   } while (i < n_tensors);
   return HSTU_OK;
 }

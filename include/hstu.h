@@ -515,7 +515,7 @@ typedef struct {
   double lr;
   double beta1;            /* [0, 1) */
   double beta2;            /* [0, 1) */
-  double eps;              /* > 0 */
+  double eps;              /* >= 2^-126 */
   int64_t step;            /* >= 1 */
   const int64_t* step_dev;
   const float* lr_dev;
