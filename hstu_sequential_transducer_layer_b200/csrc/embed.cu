@@ -32,6 +32,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortItems = 8;
 constexpr int kSortTile = kSortThreads * kSortItems;
 constexpr int kSortWarps = kSortThreads / 32;
+static_assert(kSortWarps == 32, "sort_scan");
 constexpr int kMaxCluster = 16;
 constexpr int kDigitBits = 10;  // at most; bins of one pass
 constexpr int kMaxBins = 1 << kDigitBits;
@@ -142,7 +143,7 @@ struct LookupArgs {
   int* status;
   int64_t T, R, ldt, ldo, pad;
   float scale;
-  int out_dt, d, cols;  // cols: threads along a row; blockDim.x = cols * rows per block
+  int d, cols;          // cols: threads along a row; blockDim.x = cols * rows per block
   int check;            // block 0 only validates the ids; else every block reports its own
 };
 
@@ -152,12 +153,16 @@ constexpr int64_t kCheckMax = 65536;
 // Y[t] = scale * E[ids[t]].  Bandwidth-bound; a thread keeps one column
 // group of 8 elements (1 where a row is not a multiple of 8) and walks the
 // tokens, 4 loads in flight, so that no index is divided inside the loop.
+// Both types are compiled in: with a branch on the output's type per store the
+// kernel was bound by instructions (12.5 per element).  A dropped token's
+// loads are replaced by zeros.
 // A thread of one block cannot clear the status word before another one sets
 // it, so up to kCheckMax tokens block 0 copies nothing and validates all ids
 // itself (its 8 bytes per token are read while the others copy); beyond that
 // the word is cleared by a memset before the launch.
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(256) k_embed_lookup(const LookupArgs a) {
+template <int DT, int OUT, bool VEC>
+__global__ void __launch_bounds__(256, DT == HSTU_FP32 || OUT == HSTU_FP32 ? 4 : 5)
+    k_embed_lookup(const LookupArgs a) {
   if (a.check && blockIdx.x == 0) {
     bool bad = false;
     for (int64_t t = threadIdx.x; t < a.T; t += blockDim.x) {
@@ -174,15 +179,15 @@ __global__ void __launch_bounds__(256) k_embed_lookup(const LookupArgs a) {
   const int n_cols = VEC ? a.d / 8 : a.d;
   for (int64_t t0 = block * rows * kLookupUnroll + r0; t0 < a.T;
        t0 += blocks * rows * kLookupUnroll) {
-    int64_t id[kLookupUnroll];
+    int64_t from[kLookupUnroll];  // first element of the token's row, -1: none
 #pragma unroll
     for (int u = 0; u < kLookupUnroll; ++u) {
       const int64_t t = t0 + (int64_t)u * rows;
-      id[u] = t < a.T ? a.ids[t] : -1;
-      const bool in = id[u] >= 0 && id[u] < a.R;
-      if (!a.check && t < a.T && !in && id[u] != a.pad && c0 == 0)
+      const int64_t id = t < a.T ? a.ids[t] : a.pad;
+      const bool in = id >= 0 && id < a.R;
+      if (!a.check && !in && id != a.pad && c0 == 0)
         atomicCAS(a.status, HSTU_OK, HSTU_ERR_BAD_IDS);
-      if (!in || id[u] == a.pad) id[u] = -1;
+      from[u] = in && id != a.pad ? id * a.ldt : -1;
     }
     for (int c = c0; c < n_cols; c += a.cols) {
       if (VEC) {
@@ -190,26 +195,27 @@ __global__ void __launch_bounds__(256) k_embed_lookup(const LookupArgs a) {
 #pragma unroll
         for (int u = 0; u < kLookupUnroll; ++u) {
           r[u] = Raw8<DT>{};
-          if (id[u] >= 0) load8(r[u], a.table, id[u] * a.ldt + 8 * (int64_t)c);
+          if (from[u] >= 0) load8(r[u], a.table, from[u] + 8 * c);
         }
 #pragma unroll
         for (int u = 0; u < kLookupUnroll; ++u) {
           const int64_t t = t0 + (int64_t)u * rows;
+          if (t >= a.T) break;
           float f[8];
           widen(r[u], f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = id[u] >= 0 ? f[j] * a.scale : 0.f;
-          if (t < a.T) store8(a.out_dt, a.out, t * a.ldo + 8 * (int64_t)c, f);
+          for (int j = 0; j < 8; ++j) f[j] *= a.scale;
+          store8(OUT, a.out, t * a.ldo + 8 * c, f);
         }
       } else {
         float f[kLookupUnroll];
 #pragma unroll
         for (int u = 0; u < kLookupUnroll; ++u)
-          f[u] = id[u] >= 0 ? load1<DT>(a.table, id[u] * a.ldt + c) * a.scale : 0.f;
+          f[u] = from[u] >= 0 ? load1<DT>(a.table, from[u] + c) * a.scale : 0.f;
 #pragma unroll
         for (int u = 0; u < kLookupUnroll; ++u) {
           const int64_t t = t0 + (int64_t)u * rows;
-          if (t < a.T) store1(a.out_dt, a.out, t * a.ldo + c, f[u]);
+          if (t < a.T) store1(OUT, a.out, t * a.ldo + c, f[u]);
         }
       }
     }
@@ -217,6 +223,24 @@ __global__ void __launch_bounds__(256) k_embed_lookup(const LookupArgs a) {
 }
 
 // ---------------------------------------------------------------- sort
+// Exclusive scan over the block (kSortThreads threads) of one int per thread;
+// *all receives the sum.
+DEVI int sort_scan(int v, int* s_warp, int* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // s_warp is free (previous use done)
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  const int w = s_warp[lane];  // kSortWarps == 32
+  *all = __reduce_add_sync(0xffffffffu, w);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + incl - v;
+}
+
 // Header of the gradient's workspace.
 struct SortHead {
   int32_t status;
@@ -240,7 +264,15 @@ struct SortArgs {
   int64_t* row_ids;        // compact form: the touched rows (else null)
   int64_t* n_unique;       // compact form: their number (else null)
   SortHead* head;
+  uint32_t* arrived;       // counters of the sums, cleared here
+  int n_arrived;
 };
+
+// Clears the sums' counters; block `b` of `n`.
+DEVI void clear_arrived(const SortArgs& a, int b, int n) {
+  for (int i = b * kSortThreads + threadIdx.x; i < a.n_arrived; i += n * kSortThreads)
+    a.arrived[i] = 0;
+}
 
 DEVI uint32_t token_key(const SortArgs& a, int64_t id, bool* bad) {
   const bool in = id >= 0 && id < (int64_t)a.n_rows;
@@ -361,7 +393,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const SortArgs a,
     const int b = threadIdx.x;
     const int total = b < bins ? (int)a.hist[(size_t)a.tiles * bins + b] : 0;
     int all;
-    const int base = block_excl_scan<kSortThreads>(total, s_scan, &all);
+    const int base = sort_scan(total, s_scan, &all);
     if (b < bins) s_base[b] = base + a.hist[(size_t)blockIdx.x * bins + b];
   }
   uint32_t key[kSortItems], digit[kSortItems], rank[kSortItems];
@@ -398,6 +430,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_heads(const SortArgs a) {
   __shared__ int s_scan[kSortWarps];
   grid_dep_launch();
   grid_dep_wait();
+  clear_arrived(a, blockIdx.x, gridDim.x);
   const uint32_t* key = a.key[a.passes & 1];
   int n = 0;
 #pragma unroll
@@ -406,7 +439,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_heads(const SortArgs a) {
     n += i < a.T && seg_head(key, a.n_rows, i);
   }
   int all;
-  block_excl_scan<kSortThreads>(n, s_scan, &all);
+  sort_scan(n, s_scan, &all);
   if (threadIdx.x == 0) a.heads[blockIdx.x] = all;
 }
 
@@ -420,14 +453,14 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_segments(const SortArgs a
   int before = 0;
   for (int t = threadIdx.x; t < (int)blockIdx.x; t += kSortThreads) before += a.heads[t];
   int run;
-  block_excl_scan<kSortThreads>(before, s_scan, &run);
+  sort_scan(before, s_scan, &run);
   const bool last_tile = blockIdx.x == gridDim.x - 1;
   for (int k = 0; k < kSortItems; ++k) {
     const int i = blockIdx.x * kSortTile + k * kSortThreads + threadIdx.x;
     const bool valid = i < a.T && key[i] < a.n_rows;
     const bool h = i < a.T && seg_head(key, a.n_rows, i);
     int all;
-    const int pre = block_excl_scan<kSortThreads>(h, s_scan, &all);
+    const int pre = sort_scan(h, s_scan, &all);
     if (valid) {
       const int seg = run + pre + h - 1;
       a.rank[i] = (uint32_t)seg;
@@ -456,14 +489,28 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_segments(const SortArgs a
 // pass are the cluster's own (they order global memory too), so the whole sort
 // with the segments' numbers is one launch.  The launch's other
 // clusters clear the dense gradient meanwhile (if there is one to clear): the
-// sort is bound by its barriers and leaves the memory idle.
+// sort is bound by its barriers and leaves the memory idle.  Where that leaves
+// room in the L2 cache they ask it for dY, which the sums read next.
 constexpr int64_t kClusterTokens = (int64_t)kMaxCluster * kSortTile;
 
 struct FillArgs {
   uint8_t* out;        // null: nothing to clear
   int64_t rows, row_bytes, pitch;
   int unit;            // bytes of one element
+  const uint8_t* ask;  // null: nothing to ask the L2 cache for
+  int64_t ask_bytes;   // a multiple of 16
 };
+
+constexpr int64_t kAskMost = (int64_t)96 << 20, kAskFill = (int64_t)32 << 20;
+// Asks the L2 cache for dY while the tokens are sorted.
+constexpr int kAskChunk = 4096;
+DEVI void ask_l2(const FillArgs& f, int64_t block, int64_t blocks) {
+  for (int64_t o = (block * kSortThreads + threadIdx.x) * kAskChunk; o < f.ask_bytes;
+       o += blocks * kSortThreads * kAskChunk)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(f.ask + o),
+                 "r"((uint32_t)min((int64_t)kAskChunk, f.ask_bytes - o))
+                 : "memory");
+}
 
 DEVI void fill_zero(const FillArgs& f, int64_t block, int64_t blocks) {
   if (f.row_bytes == f.pitch) {
@@ -501,9 +548,12 @@ __global__ void __launch_bounds__(kSortThreads)
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
   if ((int)blockIdx.x >= nc) {
-    fill_zero(f, (int64_t)blockIdx.x - nc, (int64_t)gridDim.x - nc);
+    const int64_t block = (int64_t)blockIdx.x - nc, blocks = (int64_t)gridDim.x - nc;
+    if (f.out) fill_zero(f, block, blocks);
+    if (f.ask) ask_l2(f, block, blocks);
     return;
   }
+  clear_arrived(a, c, nc);
   const int bins = 1 << a.digit;
   uint2* pair = reinterpret_cast<uint2*>(s_mem);  // (key, token)
   uint2* pair2 = pair + tile;
@@ -552,7 +602,7 @@ __global__ void __launch_bounds__(kSortThreads)
       }
     }
     int sum;
-    const int first = block_excl_scan<kSortThreads>((int)all, s_scan, &sum);
+    const int first = sort_scan((int)all, s_scan, &sum);
     if (tid < bins) base[tid] = (uint32_t)first + before;
     __syncthreads();
 #pragma unroll
@@ -580,7 +630,7 @@ __global__ void __launch_bounds__(kSortThreads)
       count += 0x10000 + (first || (i > 0 ? pair[i - 1].x : left) != key);
   }
   int all;
-  int seg = block_excl_scan<kSortThreads>(count, s_scan, &all) & 0xffff;
+  int seg = sort_scan(count, s_scan, &all) & 0xffff;
   const int any_bad = __syncthreads_or(bad);
   if (tid == 0) *reinterpret_cast<int4*>(a.sums + 4 * c) = make_int4(any_bad, all & 0xffff, all >> 16, 0);
   cluster.sync();  // the blocks' sums; also the last access to another block's shared memory is done
@@ -633,6 +683,7 @@ struct SumArgs {
   const void* dY;
   void* out;
   float* part;        // [runs, 2, ld_part]
+  uint32_t* arrived;  // [runs, column blocks]: blocks of the segment starting there that are done
   int64_t ld_dy, ld_out;
   float scale;
   int d, ld_part, out_dt, compact, accumulate;
@@ -676,9 +727,10 @@ DEVI void put8(float* p, int lane, const float (&f)[8]) {
   q[0] = make_float4(f[0], f[1], f[2], f[3]);
   q[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
+template <bool L2 = false>  // L2: written by another block of this launch
 DEVI void add8(const float* p, int lane, float (&f)[8]) {
   const float4* q = reinterpret_cast<const float4*>(p + 8 * lane);
-  const float4 x = q[0], y = q[1];
+  const float4 x = L2 ? __ldcg(q) : q[0], y = L2 ? __ldcg(q + 1) : q[1];
   f[0] += x.x;
   f[1] += x.y;
   f[2] += x.z;
@@ -799,42 +851,43 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const
     else
       put8(part + a.ld_part, lane, acc);
   }
-}
-
-// Joins the parts of a segment that starts in run `blockIdx.x` and goes on
-// behind it: this run's second part, then the first part of each later run
-// that it reaches, the runs split among the warps in order.
-constexpr int kJoinWarps = 16;
-template <bool VEC>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_embed_join(const SumArgs a) {
-  __shared__ float s_acc[kJoinWarps][kColumns];
-  grid_dep_wait();
-  const int live = a.head->live, segs = a.head->segs;
-  const int e = (int)min((int64_t)(blockIdx.x + 1) * kRun, (int64_t)live);
-  if (e >= live) return;
-  const uint32_t k = a.key[e - 1];
-  if (a.key[e] != k) return;
-  const uint32_t rank = a.rank[e - 1];
-  if ((int)a.seg_start[rank] < e - kRun) return;
-  const int end = (int)rank + 1 < segs ? (int)a.seg_start[rank + 1] : live;
-  const int first = blockIdx.x + 1, last = (end - 1) / kRun;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.y * kColumns;
-  const int per = (last - first + kJoinWarps) / kJoinWarps;
-  float acc[8];
+  // Segments that pass this block's borders: the last of a segment's blocks to
+  // get here joins its parts (in their order, whoever it is).  This block has
+  // part in the segment at its first position, if that began before, and in
+  // the one at its last position, if that goes on behind.
+  const int e = min(b0 + kRun, live);
+  for (int which = 0; which < 2; ++which) {
+    const uint32_t k = a.key[which == 0 ? b0 : e - 1];
+    if (which == 0 ? b0 == 0 || a.key[b0 - 1] != k : e == live || a.key[e] != k) continue;
+    const uint32_t seg = a.rank[which == 0 ? b0 : e - 1];
+    const int start = (int)a.seg_start[seg];
+    if (which == 1 && start < b0) continue;  // the same segment as at the first position
+    const int end = (int)seg + 1 < a.head->segs ? (int)a.seg_start[seg + 1] : live;
+    const int first = start / kRun, last = (end - 1) / kRun;
+    __syncthreads();  // the parts are written, and s_flags is free
+    if (threadIdx.x == 0) {
+      __threadfence();
+      s_flags[0] = (int)atomicAdd(&a.arrived[(int64_t)first * gridDim.y + blockIdx.y], 1u) ==
+                   last - first;
+    }
+    __syncthreads();
+    if (!s_flags[0]) continue;
+    __threadfence();
+    const int per = (last - first + kRunWarps) / kRunWarps;  // of the runs behind the first
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-  if (warp == 0)
-    add8(a.part + ((int64_t)blockIdx.x * 2 + 1) * a.ld_part + c0, lane, acc);
-  const int r1 = min(first + (warp + 1) * per, last + 1);
-#pragma unroll 4
-  for (int r = first + warp * per; r < r1; ++r)
-    add8(a.part + (int64_t)r * 2 * a.ld_part + c0, lane, acc);
-  put8(s_acc[warp], lane, acc);
-  __syncthreads();
-  if (warp != 0) return;
-  for (int w = 1; w < kJoinWarps; ++w) add8(s_acc[w], lane, acc);
-  write_row<VEC>(a, k, rank, c0, lane, acc);
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    if (warp == 0) add8<true>(a.part + ((int64_t)first * 2 + 1) * a.ld_part + c0, lane, acc);
+    const int r1 = min(first + 1 + (warp + 1) * per, last + 1);
+#pragma unroll 8
+    for (int r = first + 1 + warp * per; r < r1; ++r)
+      add8<true>(a.part + (int64_t)r * 2 * a.ld_part + c0, lane, acc);
+    put8(s_pre[warp], lane, acc);
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < kRunWarps; ++w) add8(s_pre[w], lane, acc);
+      write_row<VEC>(a, k, seg, c0, lane, acc);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -844,8 +897,8 @@ bool dtype_ok(int32_t t) { return t == HSTU_BF16 || t == HSTU_FP32 || t == HSTU_
 size_t dsize(int32_t t) { return t == HSTU_FP32 ? 4 : 2; }
 
 struct BwdLayout {
-  size_t head, key[2], val[2], hist, bad, heads, sums, rank, seg_start, part, total;
-  int tiles, passes, digit, runs, ld_part;
+  size_t head, key[2], val[2], hist, bad, heads, sums, rank, seg_start, arrived, part, total;
+  int tiles, passes, digit, runs, ld_part, n_arrived;
 };
 
 bool bwd_layout(int64_t T, int64_t R, int32_t d, BwdLayout* L) {
@@ -874,6 +927,8 @@ bool bwd_layout(int64_t T, int64_t R, int32_t d, BwdLayout* L) {
   L->heads = take((size_t)L->tiles * 4);
   L->rank = take((size_t)T * 4);
   L->seg_start = take((size_t)T * 4);
+  L->n_arrived = L->runs * (L->ld_part / kColumns);
+  L->arrived = take((size_t)L->n_arrived * 4);
   L->part = take((size_t)L->runs * 2 * L->ld_part * 4);
   L->total = off;
   return true;
@@ -955,9 +1010,9 @@ cudaError_t sort_tokens_cluster(const SortArgs& a, const FillArgs& f, cudaStream
   *done = false;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(k_embed_sort), (int)smem);
   if (e != cudaSuccess) return e;
-  int fill = 0;  // clusters that clear the gradient, 64 KB or more for each of their blocks
-  if (f.out) {
-    const int64_t bytes = f.rows * f.row_bytes;
+  int fill = 0;  // clusters that clear and ask, 64 KB or more for each of their blocks
+  if (f.out || f.ask) {
+    const int64_t bytes = (f.out ? f.rows * f.row_bytes : 0) + f.ask_bytes;
     fill = (int)std::min<int64_t>((bytes + 65535) / 65536 / nc + 1, num_sms() / nc - 1);
     fill = std::max(fill, 1);
   }
@@ -987,13 +1042,8 @@ cudaError_t clear_rows(const FillArgs& f, cudaStream_t s) {
 template <int DT>
 cudaError_t sum_rows(const SumArgs& a, int runs, bool vec, cudaStream_t s) {
   const dim3 grid((unsigned)runs, (unsigned)((a.d + kColumns - 1) / kColumns));
-  cudaError_t e = vec ? launch_dep(K_EMBED_SUM, k_embed_sum<DT, true>, grid, kRunWarps * 32, 0, s,
-                                   true, a)
-                      : launch_dep(K_EMBED_SUM, k_embed_sum<DT, false>, grid, kRunWarps * 32, 0, s,
-                                   true, a);
-  if (e != cudaSuccess) return e;
-  return vec ? launch_dep(K_EMBED_JOIN, k_embed_join<true>, grid, kJoinWarps * 32, 0, s, true, a)
-             : launch_dep(K_EMBED_JOIN, k_embed_join<false>, grid, kJoinWarps * 32, 0, s, true, a);
+  return vec ? launch_dep(K_EMBED_SUM, k_embed_sum<DT, true>, grid, kRunWarps * 32, 0, s, true, a)
+             : launch_dep(K_EMBED_SUM, k_embed_sum<DT, false>, grid, kRunWarps * 32, 0, s, true, a);
 }
 
 hstu_status cuda_status(cudaError_t e, const char* where) {
@@ -1027,6 +1077,12 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
     f.row_bytes = (int64_t)d * f.unit;
     f.pitch = ld_out * f.unit;
   }
+  const int64_t dy_bytes = T > 0 ? ((T - 1) * ld_dy + d) * (int64_t)dsize(dy_dt) : 0;
+  if (ld_dy < 2 * (int64_t)d && f.rows * f.row_bytes <= kAskFill) {
+    f.ask = static_cast<const uint8_t*>(dY);
+    f.ask_bytes = std::min(dy_bytes, kAskMost) / 16 * 16;
+    if (f.ask_bytes == 0) f.ask = nullptr;
+  }
   if (T == 0) {
     cudaError_t e = cudaMemsetAsync(head, 0, sizeof(SortHead), s);
     if (e == cudaSuccess && f.out) e = clear_rows(f, s);
@@ -1054,6 +1110,8 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
   q.row_ids = compact ? row_ids : nullptr;
   q.n_unique = compact ? n_unique : nullptr;
   q.head = head;
+  q.arrived = reinterpret_cast<uint32_t*>(at(L.arrived));
+  q.n_arrived = L.n_arrived;
   cudaError_t e = cudaSuccess;
   bool sorted = false;
   if (T <= kClusterTokens) e = sort_tokens_cluster(q, f, s, &sorted);
@@ -1071,6 +1129,7 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
   a.dY = dY;
   a.out = out;
   a.part = reinterpret_cast<float*>(at(L.part));
+  a.arrived = q.arrived;
   a.ld_dy = ld_dy;
   a.ld_out = ld_out;
   a.scale = scale;
@@ -1086,14 +1145,20 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
   return cuda_status(e, "embed_bwd: sums");
 }
 
-template <int DT>
+template <int DT, int OUT>
 cudaError_t lookup(const LookupArgs& a, bool vec, int threads, int grid, cudaStream_t s) {
   LaunchScope ls(K_EMBED_LOOKUP, s);
   if (vec)
-    k_embed_lookup<DT, true><<<grid, threads, 0, s>>>(a);
+    k_embed_lookup<DT, OUT, true><<<grid, threads, 0, s>>>(a);
   else
-    k_embed_lookup<DT, false><<<grid, threads, 0, s>>>(a);
+    k_embed_lookup<DT, OUT, false><<<grid, threads, 0, s>>>(a);
   return cudaGetLastError();
+}
+template <int DT>
+cudaError_t lookup(const LookupArgs& a, int out, bool vec, int threads, int grid, cudaStream_t s) {
+  return out == HSTU_BF16   ? lookup<DT, HSTU_BF16>(a, vec, threads, grid, s)
+         : out == HSTU_FP16 ? lookup<DT, HSTU_FP16>(a, vec, threads, grid, s)
+                            : lookup<DT, HSTU_FP32>(a, vec, threads, grid, s);
 }
 
 }  // namespace
@@ -1128,7 +1193,6 @@ hstu_status hstu_embed_fwd(int64_t n_tokens, const int64_t* ids, const void* tab
   a.ldo = ld_out;
   a.pad = pad_id;
   a.scale = scale;
-  a.out_dt = out_dtype;
   a.d = d;
   a.check = n_tokens <= kCheckMax;
   const bool vec = d % 8 == 0 && ld_table % 8 == 0 && ld_out % 8 == 0;
@@ -1143,9 +1207,10 @@ hstu_status hstu_embed_fwd(int64_t n_tokens, const int64_t* ids, const void* tab
     if (e != cudaSuccess) return cuda_status(e, "hstu_embed_fwd");
   }
   const int grid = (int)blocks + a.check;
-  const cudaError_t e = table_dtype == HSTU_BF16   ? lookup<HSTU_BF16>(a, vec, threads, grid, s)
-                        : table_dtype == HSTU_FP16 ? lookup<HSTU_FP16>(a, vec, threads, grid, s)
-                                                   : lookup<HSTU_FP32>(a, vec, threads, grid, s);
+  const cudaError_t e =
+      table_dtype == HSTU_BF16   ? lookup<HSTU_BF16>(a, out_dtype, vec, threads, grid, s)
+      : table_dtype == HSTU_FP16 ? lookup<HSTU_FP16>(a, out_dtype, vec, threads, grid, s)
+                                 : lookup<HSTU_FP32>(a, out_dtype, vec, threads, grid, s);
   return cuda_status(e, "hstu_embed_fwd");
 }
 

@@ -57,10 +57,9 @@ enum KernelId : int32_t {
   K_EMBED_LOOKUP = 38,
   K_EMBED_SORT = 39,
   K_EMBED_SUM = 40,
-  K_EMBED_JOIN = 41,
-  K_GRAD_NORM = 42,
-  K_ADAMW = 43,
-  K_NUM_KERNELS = 44
+  K_GRAD_NORM = 41,
+  K_ADAMW = 42,
+  K_NUM_KERNELS = 43
 };
 const char* kernel_name(int id);
 

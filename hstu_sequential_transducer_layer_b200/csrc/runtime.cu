@@ -33,7 +33,7 @@ const char* kernel_name(int id) {
       "topk_merge", "tf_ln", "tf_qkv_tc", "tf_softmax_attn_tc", "tf_oproj_tc", "tf_ffn1_tc",
       "tf_ffn2_tc", "gemm_filter_tc", "filter_merge", "attn_bwd_dkv_tc", "attn_bwd_dq_tc",
       "gemm_bwd_tc", "ln_bwd", "sum_rows", "f32_to_f16", "ln_coef", "embed_lookup", "embed_sort",
-      "embed_sum", "embed_join", "grad_norm", "adamw"};
+      "embed_sum", "grad_norm", "adamw"};
   return (id >= 0 && id < K_NUM_KERNELS) ? names[id] : "unknown";
 }
 
