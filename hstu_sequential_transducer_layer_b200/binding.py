@@ -418,16 +418,31 @@ def _need(ok: bool, where: str, what: str) -> None:
         raise HstuError(1, f"{where}: {what}")
 
 
-def _here(where: str, *tensors) -> None:
-    """Every tensor is on the current CUDA device (kernels are launched there)."""
+def _here(where: str, *tensors) -> int:
+    """The current CUDA device, which every tensor must be on (kernels are
+    launched there)."""
     import torch
+    dev = torch.cuda.current_device() if tensors[0].is_cuda else -2
     for t in tensors:
-        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        if t.get_device() != dev:
             raise HstuError(1, f"{where}: a tensor on {t.device}, not on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """_stream() without the stream object that torch would build for the
+    current stream (4 us of a call that takes 8)."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else _stream(None)
 
 
 def _rows(t, where: str, name: str) -> int:
     """Row stride of a matrix whose rows are contiguous."""
+    if t.is_contiguous() and t.dim() == 2:
+        return t.shape[1]
     _need(t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1), where,
           f"{name}: rows of a matrix, contiguous")
     return t.stride(0) if t.shape[0] > 1 else max(int(t.shape[1]), t.stride(0))
@@ -447,15 +462,17 @@ def hstu_embed_fwd(ids, table, out, workspace, scale: float = 1.0, pad_id: int =
     """out[t] = scale * table[ids[t]] (see include/hstu.h).  ids: int64 [T];
     table [R, d] and out [T, d]: bf16, fp16 or fp32, rows contiguous."""
     w = "hstu_embed_fwd"
-    _here(w, ids, table, out, workspace)
+    dev = _here(w, ids, table, out, workspace)
     _i64(ids, w, "ids")
     ldt, ldo = _rows(table, w, "table"), _rows(out, w, "out")
-    _need(out.shape[0] == ids.numel() and out.shape[1] == table.shape[1], w,
-          "out: [ids, table's columns]")
-    _check(lib().hstu_embed_fwd(ids.numel(), _ptr(ids), _ptr(table), _dtype(table, w),
-                                table.shape[0], table.shape[1], ldt, int(pad_id), float(scale),
-                                _ptr(out), _dtype(out, w), ldo, _ptr(workspace),
-                                _nbytes(workspace), _stream(stream)), w)
+    (R, d), T = table.shape, ids.numel()
+    if tuple(out.shape) != (T, d):
+        raise HstuError(1, f"{w}: out: [ids, table's columns]")
+    code = lib().hstu_embed_fwd(T, ids.data_ptr(), table.data_ptr(), _dtype(table, w), R, d, ldt,
+                                pad_id, scale, out.data_ptr(), _dtype(out, w), ldo,
+                                workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, dev))
+    if code != 0:
+        _check(code, w)
 
 
 def hstu_embed_bwd_workspace_size(n_tokens: int, n_rows: int, d: int) -> int:
@@ -470,14 +487,17 @@ def hstu_embed_bwd(ids, dY, dE, workspace, scale: float = 1.0, pad_id: int = -1,
     """dE[r] = scale * sum of dY[t] over the tokens of row r, every row of the
     table's gradient written, or added into it (see include/hstu.h)."""
     w = "hstu_embed_bwd"
-    _here(w, ids, dY, dE, workspace)
+    dev = _here(w, ids, dY, dE, workspace)
     _i64(ids, w, "ids")
     ldy, lde = _rows(dY, w, "dY"), _rows(dE, w, "dE")
-    _need(dY.shape[0] == ids.numel() and dE.shape[1] == dY.shape[1], w, "dY: [ids, dE's columns]")
-    _check(lib().hstu_embed_bwd(ids.numel(), _ptr(ids), _ptr(dY), _dtype(dY, w), ldy, dE.shape[0],
-                                dE.shape[1], int(pad_id), float(scale), 1 if accumulate else 0,
-                                _ptr(dE), _dtype(dE, w), lde, _ptr(workspace), _nbytes(workspace),
-                                _stream(stream)), w)
+    (R, d), T = dE.shape, ids.numel()
+    if tuple(dY.shape) != (T, d):
+        raise HstuError(1, f"{w}: dY: [ids, dE's columns]")
+    code = lib().hstu_embed_bwd(T, ids.data_ptr(), dY.data_ptr(), _dtype(dY, w), ldy, R, d, pad_id,
+                                scale, 1 if accumulate else 0, dE.data_ptr(), _dtype(dE, w), lde,
+                                workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, dev))
+    if code != 0:
+        _check(code, w)
 
 
 def hstu_embed_bwd_rows(ids, dY, n_rows: int, row_ids, rows, n_unique, workspace,
@@ -486,19 +506,23 @@ def hstu_embed_bwd_rows(ids, dY, n_rows: int, row_ids, rows, n_unique, workspace
     and their number n_unique (int64 [1]); row_ids and rows hold min(ids,
     n_rows) entries (see include/hstu.h)."""
     w = "hstu_embed_bwd_rows"
-    _here(w, ids, dY, row_ids, rows, n_unique, workspace)
+    dev = _here(w, ids, dY, row_ids, rows, n_unique, workspace)
     for t, name in ((ids, "ids"), (row_ids, "row_ids"), (n_unique, "n_unique")):
         _i64(t, w, name)
     ldy, ldr = _rows(dY, w, "dY"), _rows(rows, w, "rows")
-    cap = min(ids.numel(), int(n_rows))
-    _need(dY.shape[0] == ids.numel() and rows.shape[1] == dY.shape[1], w, "dY: [ids, rows' columns]")
-    _need(row_ids.numel() >= cap and rows.shape[0] >= cap and n_unique.numel() >= 1, w,
-          "row_ids, rows: min(ids, n_rows) entries")
-    _check(lib().hstu_embed_bwd_rows(ids.numel(), _ptr(ids), _ptr(dY), _dtype(dY, w), ldy,
-                                     int(n_rows), dY.shape[1], int(pad_id), float(scale),
-                                     _ptr(row_ids), _ptr(rows), _dtype(rows, w), ldr,
-                                     _ptr(n_unique), _ptr(workspace), _nbytes(workspace),
-                                     _stream(stream)), w)
+    (have, d), T = rows.shape, ids.numel()
+    cap = min(T, int(n_rows))
+    if tuple(dY.shape) != (T, d):
+        raise HstuError(1, f"{w}: dY: [ids, rows' columns]")
+    if row_ids.numel() < cap or have < cap or n_unique.numel() < 1:
+        raise HstuError(1, f"{w}: row_ids, rows: min(ids, n_rows) entries")
+    code = lib().hstu_embed_bwd_rows(T, ids.data_ptr(), dY.data_ptr(), _dtype(dY, w), ldy,
+                                     int(n_rows), d, pad_id, scale, row_ids.data_ptr(),
+                                     rows.data_ptr(), _dtype(rows, w), ldr, n_unique.data_ptr(),
+                                     workspace.data_ptr(), _nbytes(workspace),
+                                     _raw_stream(stream, dev))
+    if code != 0:
+        _check(code, w)
 
 
 class GradTensors:
@@ -592,13 +616,15 @@ def hstu_grad_norm(tensors: GradTensors, max_norm: float, out, workspace, stream
     to max_norm (NaN if the norm is not finite); see include/hstu.h."""
     import torch
     w = "hstu_grad_norm"
-    _here(w, out, workspace)
-    _need(tensors.device is None or tensors.device == out.get_device(), w,
-          "the tensors are on another device")
-    _need(out.dtype == torch.float32 and out.is_contiguous() and out.numel() >= 2, w,
-          "out: fp32 [2]")
-    _check(lib().hstu_grad_norm(tensors.array, tensors.n, float(max_norm), _ptr(out),
-                                _ptr(workspace), _nbytes(workspace), _stream(stream)), w)
+    dev = _here(w, out, workspace)
+    if tensors.device is not None and tensors.device != dev:
+        raise HstuError(1, f"{w}: the tensors are on another device")
+    if out.dtype != torch.float32 or not out.is_contiguous() or out.numel() < 2:
+        raise HstuError(1, f"{w}: out: fp32 [2]")
+    code = lib().hstu_grad_norm(tensors.array, tensors.n, max_norm, out.data_ptr(),
+                                workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, dev))
+    if code != 0:
+        _check(code, w)
 
 
 def hstu_adamw_workspace_size() -> int:
@@ -613,30 +639,31 @@ def hstu_adamw_step(tensors: AdamWTensors, workspace, lr, step, beta1: float = 0
     kernel; grad_scale: fp32 [1] on the device."""
     import torch
     w = "hstu_adamw_step"
-    _need(isinstance(tensors, AdamWTensors), w, "tensors: an AdamWTensors list")
-    _here(w, workspace)
-    _need(tensors.device is None or tensors.device == workspace.get_device(), w,
-          "the tensors are on another device")
-    a = AdamWArgs(0.0, beta1, beta2, eps, 1, None, None, None, int(seed) & ((1 << 64) - 1))
+    if not isinstance(tensors, AdamWTensors):
+        raise HstuError(1, f"{w}: tensors: an AdamWTensors list")
+    dev = _here(w, workspace)
+    if tensors.device is not None and tensors.device != dev:
+        raise HstuError(1, f"{w}: the tensors are on another device")
+    lr_dev = step_dev = None
     if isinstance(lr, torch.Tensor):
-        _here(w, lr)
-        _need(lr.dtype == torch.float32 and lr.numel() == 1, w, "lr: fp32 [1]")
-        a.lr_dev = _ptr(lr)
-    else:
-        a.lr = lr
+        lr, lr_dev = 0.0, _scalar(lr, torch.float32, w, "lr")
     if isinstance(step, torch.Tensor):
-        _here(w, step)
-        _need(step.dtype == torch.int64 and step.numel() == 1, w, "step: int64 [1]")
-        a.step_dev = _ptr(step)
-    else:
-        a.step = step
+        step, step_dev = 1, _scalar(step, torch.int64, w, "step")
     if grad_scale is not None:
-        _here(w, grad_scale)
-        _need(grad_scale.dtype == torch.float32 and grad_scale.numel() == 1, w,
-              "grad_scale: fp32 [1]")
-        a.grad_scale = _ptr(grad_scale)
-    _check(lib().hstu_adamw_step(ctypes.byref(a), tensors.array, tensors.n, _ptr(workspace),
-                                 _nbytes(workspace), _stream(stream)), w)
+        grad_scale = _scalar(grad_scale, torch.float32, w, "grad_scale")
+    a = AdamWArgs(lr, beta1, beta2, eps, step, step_dev, lr_dev, grad_scale,
+                  seed & ((1 << 64) - 1))
+    code = lib().hstu_adamw_step(ctypes.byref(a), tensors.array, tensors.n, workspace.data_ptr(),
+                                 _nbytes(workspace), _raw_stream(stream, dev))
+    if code != 0:
+        _check(code, w)
+
+
+def _scalar(t, dtype, where: str, name: str) -> int:
+    """Address of a one-element device tensor."""
+    _here(where, t)
+    _need(t.dtype == dtype and t.numel() == 1, where, f"{name}: {dtype} [1]")
+    return t.data_ptr()
 
 
 def hstu_stack_fwd(desc, n_layers, weights, B, total_tokens, max_len, offsets, X, timestamps,

@@ -19,9 +19,6 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <map>
-#include <mutex>
-#include <utility>
 
 #include "ptx.cuh"
 
@@ -241,13 +238,6 @@ DEVI int sort_scan(int v, int* s_warp, int* all) {
   return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + incl - v;
 }
 
-// Header of the gradient's workspace.
-struct SortHead {
-  int32_t status;
-  int32_t live;   // sorted positions that hold a token of a table row
-  int32_t segs;   // touched rows
-};
-
 struct SortArgs {
   const int64_t* ids;
   int64_t pad;
@@ -260,10 +250,10 @@ struct SortArgs {
   int32_t* heads;          // per tile: touched rows that start in it
   int32_t* sums;           // one-launch sort: per block (bad id seen, heads, live, -)
   uint32_t* rank;          // per sorted position: its segment
-  uint32_t* seg_start;     // per segment: its first sorted position
+  uint32_t* seg_start;     // per segment: its first sorted position; behind the last: the end
   int64_t* row_ids;        // compact form: the touched rows (else null)
   int64_t* n_unique;       // compact form: their number (else null)
-  SortHead* head;
+  int32_t* status;
   uint32_t* arrived;       // counters of the sums, cleared here
   int n_arrived;
 };
@@ -334,7 +324,7 @@ __global__ void k_sort_scan(const SortArgs a, int pass) {
     bool bad = false;
     for (int t = threadIdx.x; t < a.tiles; t += blockDim.x) bad |= a.bad[t] != 0;
     const int any = __syncthreads_or(bad);
-    if (threadIdx.x == 0) a.head->status = any ? HSTU_ERR_BAD_IDS : HSTU_OK;
+    if (threadIdx.x == 0) *a.status = any ? HSTU_ERR_BAD_IDS : HSTU_OK;
   }
 }
 
@@ -468,15 +458,11 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_segments(const SortArgs a
         a.seg_start[seg] = (uint32_t)i;
         if (a.row_ids) a.row_ids[seg] = (int64_t)key[i];
       }
-      if (i + 1 == a.T || key[i + 1] >= a.n_rows) a.head->live = i + 1;
+      if (i + 1 == a.T || key[i + 1] >= a.n_rows) a.seg_start[seg + 1] = (uint32_t)(i + 1);
     }
-    if (i == 0 && !valid) a.head->live = 0;
     run += all;
   }
-  if (last_tile && threadIdx.x == 0) {
-    a.head->segs = run;
-    if (a.n_unique) *a.n_unique = run;
-  }
+  if (last_tile && threadIdx.x == 0 && a.n_unique) *a.n_unique = run;
 }
 
 // ---------------------------------------------------------------- one-launch sort
@@ -501,7 +487,8 @@ struct FillArgs {
   int64_t ask_bytes;   // a multiple of 16
 };
 
-constexpr int64_t kAskMost = (int64_t)96 << 20, kAskFill = (int64_t)32 << 20;
+constexpr int64_t kAskMost = (int64_t)96 << 20, kAskLeast = (int64_t)4 << 20,
+                  kAskFill = (int64_t)32 << 20;
 // Asks the L2 cache for dY while the tokens are sorted.
 constexpr int kAskChunk = 4096;
 DEVI void ask_l2(const FillArgs& f, int64_t block, int64_t blocks) {
@@ -644,9 +631,8 @@ __global__ void __launch_bounds__(kSortThreads)
     if (lane == 0) {
       s_before = before;
       if (c == 0) {
-        a.head->status = bads ? HSTU_ERR_BAD_IDS : HSTU_OK;
-        a.head->live = live;
-        a.head->segs = heads;
+        *a.status = bads ? HSTU_ERR_BAD_IDS : HSTU_OK;
+        a.seg_start[heads] = (uint32_t)live;
         if (a.n_unique) *a.n_unique = heads;
       }
     }
@@ -675,7 +661,8 @@ __global__ void __launch_bounds__(kSortThreads)
 
 // ---------------------------------------------------------------- sums
 struct SumArgs {
-  const SortHead* head;
+  int T;
+  uint32_t n_rows;
   const uint32_t* key;
   const uint32_t* val;
   const uint32_t* rank;
@@ -695,7 +682,8 @@ DEVI int lane_col(int lane, int j) {
   return VEC ? 8 * lane + j : 32 * j + lane;
 }
 
-template <bool VEC>
+// PLAIN: fp32, not accumulated.
+template <bool VEC, bool PLAIN>
 DEVI void write_row(const SumArgs& a, uint32_t key, uint32_t rank, int c0, int lane,
                     const float (&acc)[8]) {
   const int64_t at = (int64_t)(a.compact ? rank : key) * a.ld_out + c0;
@@ -705,17 +693,17 @@ DEVI void write_row(const SumArgs& a, uint32_t key, uint32_t rank, int c0, int l
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       f[j] = acc[j] * a.scale;
-      if (a.accumulate) f[j] += load1_dyn(a.out_dt, a.out, at + 8 * lane + j);
+      if (!PLAIN && a.accumulate) f[j] += load1_dyn(a.out_dt, a.out, at + 8 * lane + j);
     }
-    store8(a.out_dt, a.out, at + 8 * lane, f);
+    store8(PLAIN ? HSTU_FP32 : a.out_dt, a.out, at + 8 * lane, f);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = 32 * j + lane;
       if (c0 + c < a.d) {
         float f = acc[j] * a.scale;
-        if (a.accumulate) f += load1_dyn(a.out_dt, a.out, at + c);
-        store1(a.out_dt, a.out, at + c, f);
+        if (!PLAIN && a.accumulate) f += load1_dyn(a.out_dt, a.out, at + c);
+        store1(PLAIN ? HSTU_FP32 : a.out_dt, a.out, at + c, f);
       }
     }
   }
@@ -741,83 +729,90 @@ DEVI void add8(const float* p, int lane, float (&f)[8]) {
   f[7] += y.w;
 }
 
-template <int DT, bool VEC>
+// Where a segment that passes a block's border lies.
+struct Chain {
+  uint32_t key, seg;
+  int start, end;  // sorted positions; start < 0: there is none
+};
+
+// Sums of one run of sorted positions and 256 columns.  A warp's 16 positions:
+// lane i + 1 holds position i's key, token and segment, lane 0 the key before,
+// lane 17 the key behind; one ballot tells where segments start, so the loop
+// over the tokens has no exchange but the token's number.
+template <int DT, bool VEC, bool PLAIN>
 __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const SumArgs a) {
   __shared__ float s_pre[kRunWarps][kColumns], s_post[kRunWarps][kColumns];
   __shared__ int s_flags[kRunWarps];  // 1: pre holds a part, 2: it goes on past this warp
+  __shared__ Chain s_chain[2];        // of the run's first position, and of its last one
   grid_dep_launch();
-  grid_dep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int live = a.head->live;
-  const int b0 = blockIdx.x * kRun;
-  if (b0 >= live) return;
-  const int c0 = blockIdx.y * kColumns;
-  const int p0 = b0 + warp * kRunTokens;
-  const int n = min(kRunTokens, live - p0);  // may be <= 0
-  // the warp's keys, tokens and segments, one position per lane; lane n holds the next
-  // position's key (n <= 16, so there is room)
-  uint32_t key = 0xffffffffu, val = 0, rank = 0, prev = 0xffffffffu;
-  if (n > 0) {
-    if (lane <= n && p0 + lane < live) key = a.key[p0 + lane];
-    if (lane < n) {
-      val = a.val[p0 + lane];
-      rank = a.rank[p0 + lane];
-    }
-    if (p0 > 0) prev = a.key[p0 - 1];
+  const int b0 = blockIdx.x * kRun, c0 = blockIdx.y * kColumns;
+  if (threadIdx.x < 2) s_chain[threadIdx.x].start = -1;
+  grid_dep_wait();
+  const int pos = b0 + warp * kRunTokens + lane - 1;
+  const bool mine = lane >= 1 && lane <= kRunTokens && pos < a.T;
+  const uint32_t key = lane <= kRunTokens + 1 && pos >= 0 && pos < a.T ? a.key[pos] : 0xffffffffu;
+  const uint32_t val = mine ? a.val[pos] : 0, rank = mine ? a.rank[pos] : 0;
+  const uint32_t before = __shfl_up_sync(0xffffffffu, key, 1);
+  const int n = __popc(__ballot_sync(0xffffffffu, mine && key < a.n_rows));  // the first n
+  const uint32_t heads = __ballot_sync(0xffffffffu, mine && key != before) >> 1;
+  const uint32_t last_key = __shfl_sync(0xffffffffu, key, n);
+  const bool on = n > 0 && __shfl_sync(0xffffffffu, key, n + 1) == last_key;  // behind this warp
+  bool open = n > 0 && !(heads & 1);  // the running segment began before this warp's positions
+  // the segments at the run's borders: lanes 0 and 1 read where they start and end
+  const int border = warp == 0 && open ? 0 : on && b0 + kRun == pos - lane + 1 + n ? 1 : -1;
+  int bound = 0;
+  uint32_t border_seg = 0;
+  if (border >= 0) {
+    border_seg = __shfl_sync(0xffffffffu, rank, border == 0 ? 1 : n);
+    if (lane < 2) bound = (int)a.seg_start[border_seg + lane];
   }
   float acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
   int flags = 0;
-  bool post = false;
-  uint32_t cur = 0, cur_rank = 0;
-  if (n > 0) {
-    cur = __shfl_sync(0xffffffffu, key, 0);
-    cur_rank = __shfl_sync(0xffffffffu, rank, 0);
-    bool open = cur == prev;  // the running segment began before this warp's positions
-    constexpr int kBatch = DT == HSTU_FP32 ? 4 : 8;
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
-      Raw8<DT> r[VEC ? kBatch : 1];
-      float one[VEC ? 1 : kBatch][8];
+  constexpr int kBatch = DT == HSTU_FP32 ? 2 : 4;  // 8 would spill at 64 registers: 3 us of 49 slower
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    Raw8<DT> r[VEC ? kBatch : 1];
+    float one[VEC ? 1 : kBatch][8];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int64_t t = __shfl_sync(0xffffffffu, val, (i0 + u) & 31);
-        if (VEC) {
-          r[u] = Raw8<DT>{};
-          if (i0 + u < n && c0 + 8 * lane < a.d) load8(r[u], a.dY, t * a.ld_dy + c0 + 8 * lane);
-        } else {
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t row = (int64_t)__shfl_sync(0xffffffffu, val, i0 + u + 1) * a.ld_dy + c0;
+      if (VEC) {
+        r[u] = Raw8<DT>{};
+        if (i0 + u < n && c0 + 8 * lane < a.d) load8(r[u], a.dY, row + 8 * lane);
+      } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c = c0 + 32 * j + lane;
-            one[u][j] = i0 + u < n && c < a.d ? load1<DT>(a.dY, t * a.ld_dy + c) : 0.f;
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (i0 + u < n) {
-          const uint32_t k = __shfl_sync(0xffffffffu, key, i0 + u);
-          if (k != cur) {  // the running segment ends here
-            if (open) {
-              put8(s_pre[warp], lane, acc);
-              flags = 1;
-            } else {
-              write_row<VEC>(a, cur, cur_rank, c0, lane, acc);
-            }
-            open = false;
-            cur = k;
-            cur_rank = __shfl_sync(0xffffffffu, rank, i0 + u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-          }
-          float x[8];
-          if (VEC) widen(r[u], x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] += VEC ? x[j] : one[u][j];
+        for (int j = 0; j < 8; ++j) {
+          const int c = 32 * j + lane;
+          one[u][j] = i0 + u < n && c0 + c < a.d ? load1<DT>(a.dY, row + c) : 0.f;
         }
       }
     }
-    const bool on = __shfl_sync(0xffffffffu, key, n) == cur;  // goes on behind this warp
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u;
+      if (i < n && i > 0 && (heads >> i & 1)) {  // the running segment ended with token i - 1
+        if (open) {
+          put8(s_pre[warp], lane, acc);
+          flags = 1;
+        } else {
+          write_row<VEC, PLAIN>(a, __shfl_sync(0xffffffffu, key, i),
+                                __shfl_sync(0xffffffffu, rank, i), c0, lane, acc);
+        }
+        open = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+      }
+      float x[8];
+      if (VEC) widen(r[u], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += VEC ? x[j] : one[u][j];
+    }
+  }
+  const uint32_t last_rank = __shfl_sync(0xffffffffu, rank, n);
+  bool post = false;
+  if (n > 0) {
     if (open) {
       put8(s_pre[warp], lane, acc);
       flags = on ? 3 : 1;
@@ -825,21 +820,26 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const
       put8(s_post[warp], lane, acc);
       post = true;
     } else {
-      write_row<VEC>(a, cur, cur_rank, c0, lane, acc);
+      write_row<VEC, PLAIN>(a, last_key, last_rank, c0, lane, acc);
     }
   }
   if (lane == 0) s_flags[warp] = flags;
+  if (border >= 0) {
+    const int end = __shfl_sync(0xffffffffu, bound, 1);
+    // (a segment that fills the run is the first border's; its key is also lane 0's)
+    if (lane == 0 && (border == 0 || bound >= b0))
+      s_chain[border] = Chain{border == 0 ? key : last_key, border_seg, bound, end};
+  }
   __syncthreads();
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.ld_part + c0;
   // the part that began before this block, and this warp's own segment that goes on
   for (int which = 0; which < 2; ++which) {
     if (which == 0 ? !(warp == 0 && (flags & 1)) : !post) continue;
     int w = which == 0 ? 0 : warp;
-    const bool ends_here = which == 0 && !(flags & 2);
+    bool done = which == 0 && !(flags & 2);
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     add8(which == 0 ? s_pre[0] : s_post[warp], lane, acc);
-    bool done = ends_here;
     while (!done && ++w < kRunWarps) {
       add8(s_pre[w], lane, acc);
       done = !(s_flags[w] & 2);
@@ -847,23 +847,16 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const
     if (which == 0)
       put8(part, lane, acc);
     else if (done)
-      write_row<VEC>(a, cur, cur_rank, c0, lane, acc);
+      write_row<VEC, PLAIN>(a, last_key, last_rank, c0, lane, acc);
     else
       put8(part + a.ld_part, lane, acc);
   }
   // Segments that pass this block's borders: the last of a segment's blocks to
-  // get here joins its parts (in their order, whoever it is).  This block has
-  // part in the segment at its first position, if that began before, and in
-  // the one at its last position, if that goes on behind.
-  const int e = min(b0 + kRun, live);
+  // get here joins its parts (in their order, whoever it is).
   for (int which = 0; which < 2; ++which) {
-    const uint32_t k = a.key[which == 0 ? b0 : e - 1];
-    if (which == 0 ? b0 == 0 || a.key[b0 - 1] != k : e == live || a.key[e] != k) continue;
-    const uint32_t seg = a.rank[which == 0 ? b0 : e - 1];
-    const int start = (int)a.seg_start[seg];
-    if (which == 1 && start < b0) continue;  // the same segment as at the first position
-    const int end = (int)seg + 1 < a.head->segs ? (int)a.seg_start[seg + 1] : live;
-    const int first = start / kRun, last = (end - 1) / kRun;
+    const Chain x = s_chain[which];
+    if (x.start < 0) continue;
+    const int first = x.start / kRun, last = (x.end - 1) / kRun;
     __syncthreads();  // the parts are written, and s_flags is free
     if (threadIdx.x == 0) {
       __threadfence();
@@ -885,7 +878,7 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const
     __syncthreads();
     if (warp == 0) {
       for (int w = 1; w < kRunWarps; ++w) add8(s_pre[w], lane, acc);
-      write_row<VEC>(a, k, seg, c0, lane, acc);
+      write_row<VEC, PLAIN>(a, x.key, x.seg, c0, lane, acc);
     }
   }
 }
@@ -926,7 +919,7 @@ bool bwd_layout(int64_t T, int64_t R, int32_t d, BwdLayout* L) {
   L->bad = take((size_t)L->tiles * 4);
   L->heads = take((size_t)L->tiles * 4);
   L->rank = take((size_t)T * 4);
-  L->seg_start = take((size_t)T * 4);
+  L->seg_start = take(((size_t)T + 1) * 4);
   L->n_arrived = L->runs * (L->ld_part / kColumns);
   L->arrived = take((size_t)L->n_arrived * 4);
   L->part = take((size_t)L->runs * 2 * L->ld_part * 4);
@@ -981,27 +974,6 @@ int cluster_blocks(int64_t T) {
   return n;
 }
 
-// Whether clusters of `blocks` blocks with this much shared memory fit the
-// current device (asked once per device and size).
-bool cluster_fits(int blocks, size_t smem, const cudaLaunchConfig_t& cfg) {
-  static std::mutex mu;
-  static std::map<std::pair<int, std::pair<int, size_t>>, bool> known;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  std::lock_guard<std::mutex> lk(mu);
-  const auto key = std::make_pair(dev, std::make_pair(blocks, smem));
-  const auto it = known.find(key);
-  if (it != known.end()) return it->second;
-  const void* fn = reinterpret_cast<const void*>(k_embed_sort);
-  int n = 0;
-  bool ok = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-            cudaSuccess;
-  ok = ok && cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
-  if (!ok) cudaGetLastError();
-  known[key] = ok;
-  return ok;
-}
-
 // The one-launch sort; *done = false if this device cannot run it.
 cudaError_t sort_tokens_cluster(const SortArgs& a, const FillArgs& f, cudaStream_t s, bool* done) {
   const int nc = cluster_blocks(a.T), bins = 1 << a.digit;
@@ -1027,7 +999,7 @@ cudaError_t sort_tokens_cluster(const SortArgs& a, const FillArgs& f, cudaStream
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (!cluster_fits(nc, smem, cfg)) return cudaSuccess;
+  if (!cluster_fits(reinterpret_cast<const void*>(k_embed_sort), nc, cfg)) return cudaSuccess;
   *done = true;
   LaunchScope ls(K_EMBED_SORT, s);
   return cudaLaunchKernelEx(&cfg, k_embed_sort, a, f, tile);
@@ -1042,8 +1014,10 @@ cudaError_t clear_rows(const FillArgs& f, cudaStream_t s) {
 template <int DT>
 cudaError_t sum_rows(const SumArgs& a, int runs, bool vec, cudaStream_t s) {
   const dim3 grid((unsigned)runs, (unsigned)((a.d + kColumns - 1) / kColumns));
-  return vec ? launch_dep(K_EMBED_SUM, k_embed_sum<DT, true>, grid, kRunWarps * 32, 0, s, true, a)
-             : launch_dep(K_EMBED_SUM, k_embed_sum<DT, false>, grid, kRunWarps * 32, 0, s, true, a);
+  const bool plain = a.out_dt == HSTU_FP32 && !a.accumulate;
+  auto* fn = vec ? plain ? k_embed_sum<DT, true, true> : k_embed_sum<DT, true, false>
+                 : plain ? k_embed_sum<DT, false, true> : k_embed_sum<DT, false, false>;
+  return launch_dep(K_EMBED_SUM, fn, grid, kRunWarps * 32, 0, s, true, a);
 }
 
 hstu_status cuda_status(cudaError_t e, const char* where) {
@@ -1068,7 +1042,7 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
     return HSTU_ERR_INVALID_ARG;
   if (!ws || ws_bytes < L.total || !al256(ws)) return HSTU_ERR_WORKSPACE;
   auto at = [&](size_t o) { return static_cast<uint8_t*>(ws) + o; };
-  SortHead* head = reinterpret_cast<SortHead*>(at(L.head));
+  int32_t* status = reinterpret_cast<int32_t*>(at(L.head));
   FillArgs f{};
   if (!compact && !accumulate) {
     f.out = static_cast<uint8_t*>(out);
@@ -1081,10 +1055,10 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
   if (ld_dy < 2 * (int64_t)d && f.rows * f.row_bytes <= kAskFill) {
     f.ask = static_cast<const uint8_t*>(dY);
     f.ask_bytes = std::min(dy_bytes, kAskMost) / 16 * 16;
-    if (f.ask_bytes == 0) f.ask = nullptr;
+    if (f.ask_bytes < kAskLeast) f.ask = nullptr, f.ask_bytes = 0;
   }
   if (T == 0) {
-    cudaError_t e = cudaMemsetAsync(head, 0, sizeof(SortHead), s);
+    cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int32_t), s);
     if (e == cudaSuccess && f.out) e = clear_rows(f, s);
     if (e == cudaSuccess && compact) e = cudaMemsetAsync(n_unique, 0, 8, s);
     return cuda_status(e, "embed_bwd: empty batch");
@@ -1109,7 +1083,7 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
   q.seg_start = reinterpret_cast<uint32_t*>(at(L.seg_start));
   q.row_ids = compact ? row_ids : nullptr;
   q.n_unique = compact ? n_unique : nullptr;
-  q.head = head;
+  q.status = status;
   q.arrived = reinterpret_cast<uint32_t*>(at(L.arrived));
   q.n_arrived = L.n_arrived;
   cudaError_t e = cudaSuccess;
@@ -1121,7 +1095,8 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
   }
   if (e != cudaSuccess) return cuda_status(e, "embed_bwd: sort");
   SumArgs a{};
-  a.head = head;
+  a.T = (int)T;
+  a.n_rows = (uint32_t)R;
   a.key = q.key[L.passes & 1];
   a.val = q.val[L.passes & 1];
   a.rank = q.rank;

@@ -6,6 +6,7 @@
 // a grid of resident thread blocks in turn.  The list's descriptors are
 // kernel parameters, so a step needs no copy to the device and can be
 // captured.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -22,7 +23,9 @@ constexpr int kBlockElems = HSTU_STATE_BLOCK;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 // Tensors of one launch: 120 bytes each, in 32,764 bytes of kernel parameters.
-constexpr int kMaxTensors = 256;
+// A short list takes kernels with fewer parameters: copying 30 KB of them costs
+// the launching thread about 2 us.
+constexpr int kMaxTensors = 256, kFewTensors = 32;
 
 // ---------------------------------------------------------------- gradient norm
 struct NormTensor {
@@ -36,12 +39,15 @@ struct NormTensor {
 constexpr int kNormChunk = 4096;
 constexpr int kNormThreads = 256;
 
+template <int N>
 struct NormArgs {
-  NormTensor t[kMaxTensors];
+  NormTensor t[N];
   int n;
   int64_t chunks;
   double* part;  // [gridDim.x]
   int* status;
+  double max_norm;  // one-launch form only, with out
+  float* out;
 };
 
 struct NormFinal {
@@ -78,6 +84,7 @@ DEVI float load_elem(int dtype, const void* p, int64_t i) {
                               : __half2float(static_cast<const __half*>(p)[i]);
 }
 
+// Sum over the block, in every thread; x summed in a fixed order.
 DEVI double block_sum(double x, double* s_warp) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
@@ -88,43 +95,77 @@ DEVI double block_sum(double x, double* s_warp) {
   return sum;
 }
 
-// Sum of squares, one partial sum per thread block.  Squares and sums are
-// fp64: a gradient of any finite fp32 size neither overflows nor vanishes,
-// and at 4 bytes a gradient the fp64 units keep up with the memory.
-__global__ void __launch_bounds__(kNormThreads)
-    k_norm_part(const __grid_constant__ NormArgs a) {
-  __shared__ double s_warp[kNormThreads / 32];
-  grid_dep_launch();
-  double acc = 0;
+DEVI void write_norm(double sum, double max_norm, float* out) {
+  const float norm = (float)sqrt(sum);
+  out[0] = norm;
+  // not finite: NaN, which makes the AdamW step leave everything as it is
+  out[1] = !(norm <= 3.402823466e38f) ? __int_as_float(0x7fffffff)
+           : norm > max_norm          ? (float)(max_norm / sqrt(sum))
+                                      : 1.f;
+}
+
+// Sum of squares of the chunks that fall to this group of kNormThreads
+// threads, one of `groups`; U chunks are read before the first one is used.
+// Squares and sums are fp64: a gradient of any finite fp32 size neither
+// overflows nor vanishes, and at 4 bytes a gradient the fp64 units keep up with
+// the memory (four sums per thread, so that one addition need not wait for the
+// one before).
+template <int U, int N>
+DEVI double sum_chunks(const NormArgs<N>& a, int64_t group, int64_t groups) {
+  constexpr int kVecs = kNormChunk / 4 / kNormThreads;
+  const int tid = threadIdx.x % kNormThreads;
+  double acc[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) acc[u] = 0;
   int t = 0;
-  for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    while (t + 1 < a.n && c >= a.t[t + 1].chunk0) ++t;
-    const NormTensor& q = a.t[t];
-    int64_t n = q.n;
-    if (q.n_rows) {
-      n = min(max(*q.n_rows, (int64_t)0), q.max_rows) * q.row_len;
-    }
-    const int64_t e0 = (c - q.chunk0) * kNormChunk;
-    const int m = (int)min((int64_t)kNormChunk, n - e0);  // may be <= 0
-    const int per = q.dtype == HSTU_FP32 ? 4 : 8;
-    const int vecs = m > 0 ? m / per : 0;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        static_cast<const uint8_t*>(q.grad) + e0 * (q.dtype == HSTU_FP32 ? 4 : 2));
-    uint4 r[kNormChunk / 4 / kNormThreads];
+  for (int64_t c0 = group; c0 < a.chunks; c0 += groups * U) {
+    uint4 r[U][kVecs];
+    int dtype[U];
+    float last[U];
 #pragma unroll
-    for (int u = 0; u < kNormChunk / 4 / kNormThreads; ++u) {
-      const int v = u * kNormThreads + threadIdx.x;
-      r[u] = v < vecs ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < U; ++k) {
+      const int64_t c = c0 + k * groups;
+      const bool in = c < a.chunks;
+      while (in && t + 1 < a.n && c >= a.t[t + 1].chunk0) ++t;
+      const NormTensor& q = a.t[t];
+      dtype[k] = q.dtype;
+      int64_t n = q.n;
+      if (q.n_rows) n = min(max(*q.n_rows, (int64_t)0), q.max_rows) * q.row_len;
+      const int64_t e0 = (c - q.chunk0) * kNormChunk;
+      const int m = in ? (int)min((int64_t)kNormChunk, n - e0) : 0;  // may be <= 0
+      const int per = dtype[k] == HSTU_FP32 ? 4 : 8;
+      const int vecs = m > 0 ? m / per : 0;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint8_t*>(q.grad) + e0 * (dtype[k] == HSTU_FP32 ? 4 : 2));
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) {
+        const int v = u * kNormThreads + tid;
+        r[k][u] = v < vecs ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+      }
+      const int tail = vecs * per + tid;
+      last[k] = tid < 8 && tail < m ? load_elem(dtype[k], q.grad, e0 + tail) : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < kNormChunk / 4 / kNormThreads; ++u) add_squares(acc, q.dtype, r[u]);
-    const int tail = vecs * per + threadIdx.x;
-    if (threadIdx.x < 8 && tail < m) {
-      const double x = load_elem(q.dtype, q.grad, e0 + tail);
-      acc = fma(x, x, acc);
+    for (int k = 0; k < U; ++k) {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) add_squares(acc[u], dtype[k], r[k][u]);
+      const double x = last[k];
+      acc[0] = fma(x, x, acc[0]);
     }
   }
-  const double sum = block_sum(acc, s_warp);
+  double sum = 0;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) sum += acc[u];
+  return sum;
+}
+
+// One partial sum per thread block.
+template <int N>
+__global__ void __launch_bounds__(kNormThreads)
+    k_norm_part(const __grid_constant__ NormArgs<N> a) {
+  __shared__ double s_warp[kNormThreads / 32];
+  grid_dep_launch();
+  const double sum = block_sum(sum_chunks<2>(a, blockIdx.x, gridDim.x), s_warp);
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = HSTU_OK;
 }
@@ -135,14 +176,38 @@ __global__ void __launch_bounds__(1024) k_norm_final(const NormFinal a) {
   double x = 0;
   for (int i = threadIdx.x; i < a.parts; i += blockDim.x) x += a.part[i];
   const double sum = block_sum(x, s_warp);
-  if (threadIdx.x == 0) {
-    const float norm = (float)sqrt(sum);
-    a.out[0] = norm;
-    // not finite: NaN, which makes the AdamW step leave everything as it is
-    a.out[1] = !(norm <= 3.402823466e38f) ? __int_as_float(0x7fffffff)
-               : norm > a.max_norm        ? (float)(a.max_norm / sqrt(sum))
-                                          : 1.f;
+  if (threadIdx.x == 0) write_norm(sum, a.max_norm, a.out);
+}
+
+// The whole norm in one launch, by one cluster of 16 blocks, where that is
+// little work: a second launch costs the host more than the other SMs would
+// save (up to 4 MB of gradients).
+constexpr int kNormCluster = 16;
+constexpr int kNormGroups = 4;  // groups of kNormThreads threads per block
+template <int N>
+__global__ void __launch_bounds__(kNormThreads * kNormGroups)
+    k_norm_small(const __grid_constant__ NormArgs<N> a) {
+  namespace cg = cooperative_groups;
+  __shared__ double s_warp[kNormThreads * kNormGroups / 32], s_sum;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int block = (int)cluster.block_rank();
+  const double x = sum_chunks<2>(a, block * kNormGroups + threadIdx.x / kNormThreads,
+                                 kNormCluster * kNormGroups);
+  const double sum = block_sum(x, s_warp);
+  if (threadIdx.x == 0) s_sum = sum;
+  cluster.sync();
+  if (block == 0 && threadIdx.x < 32) {
+    const double x =
+        threadIdx.x < kNormCluster ? *cluster.map_shared_rank(&s_sum, threadIdx.x) : 0;
+    double all = 0;
+#pragma unroll
+    for (int r = 0; r < kNormCluster; ++r) all += __shfl_sync(0xffffffffu, x, r);
+    if (threadIdx.x == 0) {
+      write_norm(all, a.max_norm, a.out);
+      *a.status = HSTU_OK;
+    }
   }
+  cluster.sync();  // no block leaves while its sum is read
 }
 
 // ---------------------------------------------------------------- AdamW
@@ -167,8 +232,9 @@ struct StepTensor {
   uint8_t kind;            // 2 * (8-bit states) + (gradient and parameter read are fp32)
 };
 
+template <int N>
 struct StepArgs {
-  StepTensor t[kMaxTensors];
+  StepTensor t[N];
   int n, first;            // tensors of this launch; number of the first one in the caller's list
   int64_t chunks;
   float b1, omb1, b2, omb2, eps;
@@ -182,7 +248,7 @@ struct StepArgs {
   int set_ok;              // nothing in this call can fail on the device: block 0 writes HSTU_OK
 };
 
-static_assert(sizeof(StepArgs) <= 32764, "kernel parameters");
+static_assert(sizeof(StepArgs<kMaxTensors>) <= 32764, "kernel parameters");
 
 // The 32-bit integer mix of C. Wellons' hash prospector ("lowbias32").
 DEVI uint32_t mix32(uint32_t x) {
@@ -573,9 +639,9 @@ DEVI bool row_block(const StepTensor& q, int64_t b, int* status, BlockAt& at) {
 // thread blocks evens out what a fixed share does not); 8-bit states, bound by
 // instructions as much as by memory, 7 resident and launched (160 us; 8
 // resident at 64 registers, which spill, 171; 6 164).
-template <bool S8, bool FAST>
+template <bool S8, bool FAST, int N>
 __global__ void __launch_bounds__(kThreads, S8 ? 7 : 6)
-    k_adamw(const __grid_constant__ StepArgs a) {
+    k_adamw(const __grid_constant__ StepArgs<N> a) {
   __shared__ StepConst s_k;
   __shared__ float s_lr;
   __shared__ int s_skip;
@@ -697,8 +763,142 @@ int64_t tensor_blocks(const hstu_adamw_tensor& t) {
   return t.row_ids ? t.max_rows * up_blocks(t.row_len) : up_blocks(t.n);
 }
 
-constexpr int kNormBlocksPerSm = 8;
+constexpr int kNormBlocksPerSm = 4;
 constexpr int kNormMaxParts = 148 * kNormBlocksPerSm * 8;
+constexpr int64_t kNormSmallChunks = 256;  // of 4096 elements
+
+template <int N>
+hstu_status grad_norm(const hstu_adamw_tensor* tensors, int n_tensors, double max_norm, float* out,
+                      void* ws, cudaStream_t s) {
+  double* part = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 256);
+  const int launches = std::max(1, (n_tensors + N - 1) / N);
+  const int most = std::min(num_sms() * kNormBlocksPerSm, kNormMaxParts / launches);
+  int parts = 0;
+  cudaLaunchAttribute at[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  for (int l = 0; l < launches; ++l) {
+    NormArgs<N> a;
+    a.n = 0;
+    a.chunks = 0;
+    for (int i = l * N; i < std::min(n_tensors, (l + 1) * N); ++i) {
+      const hstu_adamw_tensor& t = tensors[i];
+      NormTensor& q = a.t[a.n];
+      q.n = t.n_rows ? t.max_rows * t.row_len : t.n;
+      if (q.n == 0) continue;
+      q.grad = t.grad;
+      q.n_rows = t.n_rows;
+      q.row_len = t.row_len;
+      q.max_rows = t.max_rows;
+      q.dtype = t.grad_dtype;
+      q.chunk0 = a.chunks;
+      a.chunks += (q.n + kNormChunk - 1) / kNormChunk;
+      ++a.n;
+    }
+    a.part = part + parts;
+    a.status = static_cast<int*>(ws);
+    a.max_norm = max_norm;
+    a.out = out;
+    LaunchScope ls(K_GRAD_NORM, s);
+    cudaError_t e;
+    if (launches == 1 && a.chunks <= kNormSmallChunks) {
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = kNormCluster;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(kNormCluster);
+      cfg.blockDim = dim3(kNormThreads * kNormGroups);
+      if (cluster_fits(reinterpret_cast<const void*>(k_norm_small<N>), kNormCluster, cfg))
+        return cuda_status(cudaLaunchKernelEx(&cfg, k_norm_small<N>, a), "hstu_grad_norm");
+    }
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(a.chunks, most));
+    parts += grid;
+    k_norm_part<N><<<grid, kNormThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_status(e, "hstu_grad_norm");
+  }
+  NormFinal f{part, parts, max_norm, out};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  LaunchScope ls(K_GRAD_NORM, s);
+  return cuda_status(cudaLaunchKernelEx(&cfg, k_norm_final, f), "hstu_grad_norm");
+}
+
+template <int N>
+hstu_status adamw(const hstu_adamw_args& h, const hstu_adamw_tensor* tensors, int n_tensors,
+                  bool fails, bool large, void* ws, cudaStream_t s) {
+  StepArgs<N> a;
+  a.b1 = (float)h.beta1;
+  a.omb1 = (float)(1.0 - h.beta1);
+  a.b2 = (float)h.beta2;
+  a.omb2 = (float)(1.0 - h.beta2);
+  a.eps = (float)h.eps;
+  a.log_b1 = std::log(h.beta1);
+  a.log_b2 = std::log(h.beta2);
+  a.bc1 = -std::expm1((double)h.step * a.log_b1);
+  a.bc2 = -std::expm1((double)h.step * a.log_b2);
+  a.lr = h.lr;
+  a.step = h.step;
+  a.step_dev = h.step_dev;
+  a.lr_dev = h.lr_dev;
+  a.grad_scale = h.grad_scale;
+  a.seed = h.seed;
+  a.status = static_cast<int*>(ws);
+  a.set_ok = !fails;
+  int i = 0;
+  do {
+    a.first = i;
+    a.n = 0;
+    a.chunks = 0;
+    for (; i < n_tensors && a.n < N; ++i) {
+      const hstu_adamw_tensor& t = tensors[i];
+      StepTensor& q = a.t[a.n++];
+      q.grad = t.grad;
+      q.param = t.param;
+      q.master = t.param_dtype == HSTU_FP32 ? nullptr : t.master;
+      q.copy = static_cast<__half*>(t.copy_f16);
+      q.m = t.m;
+      q.v = t.v;
+      q.m_scale = t.m_scale;
+      q.v_scale = t.v_scale;
+      q.row_ids = t.row_ids;
+      q.n_rows = t.n_rows;
+      q.n = t.n;
+      q.rows = t.row_ids ? t.n / t.row_len : 0;
+      q.row_len = t.row_ids ? (int32_t)t.row_len : 0;
+      q.row_blocks = t.row_ids ? (int32_t)up_blocks(t.row_len) : 0;
+      q.max_rows = (int32_t)t.max_rows;
+      q.chunk0 = (int32_t)a.chunks;
+      q.weight_decay = (float)t.weight_decay;
+      q.grad_dtype = (uint8_t)t.grad_dtype;
+      q.param_dtype = (uint8_t)t.param_dtype;
+      q.kind = (uint8_t)(2 * (t.state_bits == 8) +
+                         (t.grad_dtype == HSTU_FP32 && (q.master || t.param_dtype == HSTU_FP32)));
+      q.per = large && t.state_bits == 8 && !t.row_ids ? kPerWarp : 1;
+      const int64_t chunk = kWarps * q.per;
+      a.chunks += (tensor_blocks(t) + chunk - 1) / chunk;
+    }
+    // a kernel per kind of tensor: one list seldom has more than one or two
+    unsigned kinds = a.n == 0 ? 1u : 0u;
+    for (int j = 0; j < a.n; ++j) kinds |= 1u << a.t[j].kind;
+    static void (*const fn[4])(StepArgs<N>) = {
+        k_adamw<false, false, N>, k_adamw<false, true, N>, k_adamw<true, false, N>,
+        k_adamw<true, true, N>};
+    for (int j = 0; j < 4; ++j) {
+      if (!(kinds >> j & 1)) continue;
+      LaunchScope ls(K_ADAMW, s);
+      const int grid = (int)std::max<int64_t>(
+          1, std::min<int64_t>(a.chunks, num_sms() * (j >= 2 ? 7 : 16)));
+      fn[j]<<<grid, kThreads, 0, s>>>(a);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");
+    }
+  } while (i < n_tensors);
+  return HSTU_OK;
+}
 
 }  // namespace
 }  // namespace hstu
@@ -719,50 +919,9 @@ hstu_status hstu_grad_norm(const hstu_adamw_tensor* tensors, int32_t n_tensors, 
   for (int i = 0; i < n_tensors; ++i)
     if (!grad_ok(tensors[i], &sparse)) return HSTU_ERR_INVALID_ARG;
   if (!ws || ws_bytes < hstu_grad_norm_workspace_size() || !al256(ws)) return HSTU_ERR_WORKSPACE;
-  double* part = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 256);
-  const int launches = std::max(1, (n_tensors + kMaxTensors - 1) / kMaxTensors);
-  const int most = std::min(num_sms() * kNormBlocksPerSm, kNormMaxParts / launches);
-  int parts = 0;
-  for (int l = 0; l < launches; ++l) {
-    NormArgs a;
-    a.n = 0;
-    a.chunks = 0;
-    for (int i = l * kMaxTensors; i < std::min(n_tensors, (l + 1) * kMaxTensors); ++i) {
-      const hstu_adamw_tensor& t = tensors[i];
-      grad_ok(t, &sparse);
-      NormTensor& q = a.t[a.n];
-      q.n = sparse ? t.max_rows * t.row_len : t.n;
-      if (q.n == 0) continue;
-      q.grad = t.grad;
-      q.n_rows = t.n_rows;
-      q.row_len = t.row_len;
-      q.max_rows = t.max_rows;
-      q.dtype = t.grad_dtype;
-      q.chunk0 = a.chunks;
-      a.chunks += (q.n + kNormChunk - 1) / kNormChunk;
-      ++a.n;
-    }
-    a.part = part + parts;
-    a.status = static_cast<int*>(ws);
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(a.chunks, most));
-    parts += grid;
-    LaunchScope ls(K_GRAD_NORM, s);
-    k_norm_part<<<grid, kNormThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_status(e, "hstu_grad_norm");
-  }
-  NormFinal f{part, parts, max_norm, out};
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  LaunchScope ls(K_GRAD_NORM, s);
-  return cuda_status(cudaLaunchKernelEx(&cfg, k_norm_final, f), "hstu_grad_norm");
+  return n_tensors <= kFewTensors
+             ? grad_norm<kFewTensors>(tensors, n_tensors, max_norm, out, ws, s)
+             : grad_norm<kMaxTensors>(tensors, n_tensors, max_norm, out, ws, s);
 }
 
 size_t hstu_adamw_workspace_size(void) { return 256; }
@@ -801,75 +960,10 @@ hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor
     const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), s);
     if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");
   }
-  StepArgs a;
-  a.b1 = (float)h.beta1;
-  a.omb1 = (float)(1.0 - h.beta1);
-  a.b2 = (float)h.beta2;
-  a.omb2 = (float)(1.0 - h.beta2);
-  a.eps = (float)h.eps;
-  a.log_b1 = std::log(h.beta1);
-  a.log_b2 = std::log(h.beta2);
-  a.bc1 = -std::expm1((double)h.step * a.log_b1);
-  a.bc2 = -std::expm1((double)h.step * a.log_b2);
-  a.lr = h.lr;
-  a.step = h.step;
-  a.step_dev = h.step_dev;
-  a.lr_dev = h.lr_dev;
-  a.grad_scale = h.grad_scale;
-  a.seed = h.seed;
-  a.status = static_cast<int*>(ws);
-  a.set_ok = !fails;
   // one block at a time where more would leave warps without work
   const bool large = blocks >= (int64_t)num_sms() * 32 * kPerWarp * 2;
-  int i = 0;
-  do {
-    a.first = i;
-    a.n = 0;
-    a.chunks = 0;
-    for (; i < n_tensors && a.n < kMaxTensors; ++i) {
-      const hstu_adamw_tensor& t = tensors[i];
-      StepTensor& q = a.t[a.n++];
-      q.grad = t.grad;
-      q.param = t.param;
-      q.master = t.param_dtype == HSTU_FP32 ? nullptr : t.master;
-      q.copy = static_cast<__half*>(t.copy_f16);
-      q.m = t.m;
-      q.v = t.v;
-      q.m_scale = t.m_scale;
-      q.v_scale = t.v_scale;
-      q.row_ids = t.row_ids;
-      q.n_rows = t.n_rows;
-      q.n = t.n;
-      q.rows = t.row_ids ? t.n / t.row_len : 0;
-      q.row_len = t.row_ids ? (int32_t)t.row_len : 0;
-      q.row_blocks = t.row_ids ? (int32_t)up_blocks(t.row_len) : 0;
-      q.max_rows = (int32_t)t.max_rows;
-      q.chunk0 = (int32_t)a.chunks;
-      q.weight_decay = (float)t.weight_decay;
-      q.grad_dtype = (uint8_t)t.grad_dtype;
-      q.param_dtype = (uint8_t)t.param_dtype;
-      q.kind = (uint8_t)(2 * (t.state_bits == 8) +
-                         (t.grad_dtype == HSTU_FP32 && (q.master || t.param_dtype == HSTU_FP32)));
-      q.per = large && t.state_bits == 8 && !t.row_ids ? kPerWarp : 1;
-      const int64_t chunk = kWarps * q.per;
-      a.chunks += (tensor_blocks(t) + chunk - 1) / chunk;
-    }
-    // a kernel per kind of tensor: one list seldom has more than one or two
-    unsigned kinds = a.n == 0 ? 1u : 0u;
-    for (int j = 0; j < a.n; ++j) kinds |= 1u << a.t[j].kind;
-    static void (*const fn[4])(StepArgs) = {k_adamw<false, false>, k_adamw<false, true>,
-                                            k_adamw<true, false>, k_adamw<true, true>};
-    for (int j = 0; j < 4; ++j) {
-      if (!(kinds >> j & 1)) continue;
-      LaunchScope ls(K_ADAMW, s);
-      const int grid = (int)std::max<int64_t>(
-          1, std::min<int64_t>(a.chunks, num_sms() * (j >= 2 ? 7 : 16)));
-      fn[j]<<<grid, kThreads, 0, s>>>(a);
-      const cudaError_t e = cudaGetLastError();
-      if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");
-    }
-  } while (i < n_tensors);
-  return HSTU_OK;
+  return n_tensors <= kFewTensors ? adamw<kFewTensors>(h, tensors, n_tensors, fails, large, ws, s)
+                                  : adamw<kMaxTensors>(h, tensors, n_tensors, fails, large, ws, s);
 }
 
 }  // extern "C"

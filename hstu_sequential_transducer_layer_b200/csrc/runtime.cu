@@ -5,6 +5,7 @@
 #include <cstring>
 #include <mutex>
 #include <map>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -69,6 +70,24 @@ cudaError_t ensure_smem_limit(const void* fn, int bytes) {
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) set_to[key] = bytes;
   return e;
+}
+
+bool cluster_fits(const void* fn, int blocks, const cudaLaunchConfig_t& cfg) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int, size_t>, bool> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_tuple(fn, dev, blocks, cfg.dynamicSmemBytes);
+  const auto it = known.find(key);
+  if (it != known.end()) return it->second;
+  int n = 0;
+  const bool ok =
+      cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
+  if (!ok) cudaGetLastError();
+  known[key] = ok;
+  return ok;
 }
 
 // ---------------------------------------------------------------- wait test hook
