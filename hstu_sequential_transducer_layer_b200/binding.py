@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
@@ -171,7 +172,7 @@ def lib() -> ctypes.CDLL:
     L.hstu_embed_bwd_rows.restype = i32
     L.hstu_grad_norm.argtypes = [pt, i32, ctypes.c_double, vp, vp, sz, vp]
     L.hstu_grad_norm.restype = i32
-    L.hstu_adamw_step.argtypes = [ctypes.POINTER(AdamWArgs), pt, i32, vp, sz, vp]
+    L.hstu_adamw_step.argtypes = [vp, pt, i32, vp, sz, vp]  # hstu_adamw_args, packed or by address
     L.hstu_adamw_step.restype = i32
     L.hstu_read_status.argtypes = [vp, sz, vp]
     L.hstu_read_status.restype = i32
@@ -399,14 +400,25 @@ def hstu_sl_embed_ids(B, raw_total, max_raw_len, raw_offsets, raw_ids, raw_times
 
 
 # ------------------------------------------------------ embedding and optimizer
-_DTYPES = None
+# Small calls are bound by this file's own time: what every one of them needs
+# of torch is looked up once (_torch_names).
+_DTYPES = _FP32 = _INT64 = _current_device = _current_raw_stream = None
+
+
+def _torch_names() -> None:
+    global _DTYPES, _FP32, _INT64, _current_device, _current_raw_stream
+    import torch
+    _FP32, _INT64, _current_device = torch.float32, torch.int64, torch.cuda.current_device
+    # the stream's address without the stream object that torch.cuda.current_stream() builds
+    # (4 us of a call that takes 8)
+    _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _DTYPES = {torch.bfloat16: HSTU_BF16, torch.float32: HSTU_FP32, torch.float16: HSTU_FP16}
 
 
 def _dtype(t, where: str) -> int:
-    global _DTYPES
     if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.bfloat16: HSTU_BF16, torch.float32: HSTU_FP32, torch.float16: HSTU_FP16}
+        _torch_names()
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise HstuError(2, f"{where}: {t.dtype} tensor")
@@ -421,8 +433,9 @@ def _need(ok: bool, where: str, what: str) -> None:
 def _here(where: str, *tensors) -> int:
     """The current CUDA device, which every tensor must be on (kernels are
     launched there)."""
-    import torch
-    dev = torch.cuda.current_device() if tensors[0].is_cuda else -2
+    if _DTYPES is None:
+        _torch_names()
+    dev = _current_device() if tensors[0].is_cuda else -2
     for t in tensors:
         if t.get_device() != dev:
             raise HstuError(1, f"{where}: a tensor on {t.device}, not on the current CUDA device")
@@ -430,13 +443,7 @@ def _here(where: str, *tensors) -> int:
 
 
 def _raw_stream(stream, dev: int) -> int:
-    """_stream() without the stream object that torch would build for the
-    current stream (4 us of a call that takes 8)."""
-    if stream is not None:
-        return _stream(stream)
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(dev) if raw is not None else _stream(None)
+    return _current_raw_stream(dev) if stream is None else _stream(stream)
 
 
 def _rows(t, where: str, name: str) -> int:
@@ -449,8 +456,10 @@ def _rows(t, where: str, name: str) -> int:
 
 
 def _i64(t, where: str, name: str) -> None:
-    import torch
-    _need(t.dtype == torch.int64 and t.is_contiguous(), where, f"{name}: a contiguous int64 tensor")
+    if _DTYPES is None:
+        _torch_names()
+    if t.dtype != _INT64 or not t.is_contiguous():
+        raise HstuError(1, f"{where}: {name}: a contiguous int64 tensor")
 
 
 def hstu_embed_workspace_size() -> int:
@@ -614,12 +623,11 @@ def hstu_grad_norm_workspace_size() -> int:
 def hstu_grad_norm(tensors: GradTensors, max_norm: float, out, workspace, stream=None) -> None:
     """out (fp32 [2]): the norm over all gradients, and the factor that clips it
     to max_norm (NaN if the norm is not finite); see include/hstu.h."""
-    import torch
     w = "hstu_grad_norm"
     dev = _here(w, out, workspace)
     if tensors.device is not None and tensors.device != dev:
         raise HstuError(1, f"{w}: the tensors are on another device")
-    if out.dtype != torch.float32 or not out.is_contiguous() or out.numel() < 2:
+    if out.dtype != _FP32 or not out.is_contiguous() or out.numel() < 2:
         raise HstuError(1, f"{w}: out: fp32 [2]")
     code = lib().hstu_grad_norm(tensors.array, tensors.n, max_norm, out.data_ptr(),
                                 workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, dev))
@@ -637,32 +645,35 @@ def hstu_adamw_step(tensors: AdamWTensors, workspace, lr, step, beta1: float = 0
     """One AdamW step of every tensor of the list (see include/hstu.h).  `lr`
     and `step` are numbers, or device tensors (fp32 [1], int64 [1]) read by the
     kernel; grad_scale: fp32 [1] on the device."""
-    import torch
     w = "hstu_adamw_step"
     if not isinstance(tensors, AdamWTensors):
         raise HstuError(1, f"{w}: tensors: an AdamWTensors list")
     dev = _here(w, workspace)
     if tensors.device is not None and tensors.device != dev:
         raise HstuError(1, f"{w}: the tensors are on another device")
-    lr_dev = step_dev = None
-    if isinstance(lr, torch.Tensor):
-        lr, lr_dev = 0.0, _scalar(lr, torch.float32, w, "lr")
-    if isinstance(step, torch.Tensor):
-        step, step_dev = 1, _scalar(step, torch.int64, w, "step")
+    lr_dev = step_dev = scale = 0
+    if hasattr(lr, "data_ptr"):
+        lr, lr_dev = 0.0, _scalar(lr, _FP32, w, "lr", dev)
+    if hasattr(step, "data_ptr"):
+        step, step_dev = 1, _scalar(step, _INT64, w, "step", dev)
     if grad_scale is not None:
-        grad_scale = _scalar(grad_scale, torch.float32, w, "grad_scale")
-    a = AdamWArgs(lr, beta1, beta2, eps, step, step_dev, lr_dev, grad_scale,
-                  seed & ((1 << 64) - 1))
-    code = lib().hstu_adamw_step(ctypes.byref(a), tensors.array, tensors.n, workspace.data_ptr(),
-                                 _nbytes(workspace), _raw_stream(stream, dev))
+        scale = _scalar(grad_scale, _FP32, w, "grad_scale", dev)
+    # hstu_adamw_args
+    args = _pack_args(lr, beta1, beta2, eps, step, step_dev, lr_dev, scale, seed & ((1 << 64) - 1))
+    code = lib().hstu_adamw_step(args, tensors.array, tensors.n, workspace.data_ptr(),
+                                 _nbytes(workspace), _current_raw_stream(dev) if stream is None
+                                 else _stream(stream))
     if code != 0:
         _check(code, w)
 
 
-def _scalar(t, dtype, where: str, name: str) -> int:
+_pack_args = struct.Struct("4dq4Q").pack
+
+
+def _scalar(t, dtype, where: str, name: str, dev: int) -> int:
     """Address of a one-element device tensor."""
-    _here(where, t)
-    _need(t.dtype == dtype and t.numel() == 1, where, f"{name}: {dtype} [1]")
+    if t.get_device() != dev or t.dtype != dtype or t.numel() != 1:
+        raise HstuError(1, f"{where}: {name}: {dtype} [1] on the current device")
     return t.data_ptr()
 
 

@@ -330,22 +330,28 @@ __global__ void k_sort_scan(const SortArgs a, int pass) {
 
 // Ranks a tile's items among those of the same digit, in tile order: each
 // warp counts its own 32 * items consecutive items (equal digits of one
-// 32-item step found by match), then the warps' counts are summed up per
-// digit.  On return hist[w][b] is the number of items of digit b in warps
+// 32-item step found by match: 850 cycles a step of 32 warps, against 1300 with
+// one ballot per bit), then the warps' counts are summed up per digit.  On return hist[w][b] is the number of items of digit b in warps
 // before w, rank[k] this thread's item's number inside its warp, and total[b]
-// (if given) the tile's number of items of digit b.
+// (if given) the tile's number of items of digits 2 b (low half) and 2 b + 1.
+// Every warp's counts (its row of hist) must be zero before.
+DEVI void clear_counts(uint16_t* hist, int bits) {
+  const int row = 2 << bits;  // bytes
+  uint8_t* mine = reinterpret_cast<uint8_t*>(hist) + (threadIdx.x >> 5) * row;
+  for (int i = 4 * (threadIdx.x & 31); i < row; i += 128)
+    *reinterpret_cast<uint32_t*>(mine + i) = 0;
+  __syncwarp();
+}
 DEVI void rank_tile(const uint32_t (&digit)[kSortItems], const bool (&in)[kSortItems], int items,
-                    int bins, uint16_t* hist, uint32_t (&rank)[kSortItems], uint32_t* total) {
+                    int bits, uint16_t* hist, uint32_t (&rank)[kSortItems], uint32_t* total) {
+  const int bins = 1 << bits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * bins / 8; i += kSortThreads)
-    reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
   uint16_t* mine = hist + warp * bins;
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     if (k >= items) break;
-    const uint32_t d = in[k] ? digit[k] : 0xffffffffu;
-    const uint32_t peers = __match_any_sync(0xffffffffu, d);
+    const uint32_t d = digit[k];
+    const uint32_t peers = __match_any_sync(0xffffffffu, in[k] ? d : 0xffffffffu);
     const uint32_t before = in[k] ? mine[d] : 0;
     rank[k] = before + __popc(peers & ((1u << lane) - 1));
     __syncwarp();
@@ -363,10 +369,7 @@ DEVI void rank_tile(const uint32_t (&digit)[kSortItems], const bool (&in)[kSortI
       two[w * (bins / 2) + b] = sum;
       sum += n;
     }
-    if (total) {
-      total[2 * b] = sum & 0xffffu;
-      total[2 * b + 1] = sum >> 16;
-    }
+    if (total) total[b] = sum;
   }
   __syncthreads();
 }
@@ -397,7 +400,8 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const SortArgs a,
     key[k] = in[k] ? src[i] : 0;
     digit[k] = (key[k] >> shift) & (bins - 1);
   }
-  rank_tile(digit, in, kSortItems, bins, s_warp_hist, rank, nullptr);
+  clear_counts(s_warp_hist, a.digit);
+  rank_tile(digit, in, kSortItems, a.digit, s_warp_hist, rank, nullptr);
   uint32_t* dst_key = a.key[(pass + 1) & 1];
   uint32_t* dst_val = a.val[(pass + 1) & 1];
 #pragma unroll
@@ -560,6 +564,7 @@ __global__ void __launch_bounds__(kSortThreads)
       in[k] = k < items && w0 + 32 * k < n;
       id[k] = in[k] ? a.ids[c * tile + w0 + 32 * k] : 0;
     }
+    clear_counts(hist, a.digit);
 #pragma unroll
     for (int k = 0; k < kSortItems; ++k) {
       bool b;
@@ -574,23 +579,28 @@ __global__ void __launch_bounds__(kSortThreads)
       if (p > 0) x[k] = in[k] ? pair[w0 + 32 * k] : make_uint2(0, 0);
       digit[k] = (x[k].x >> (p * a.digit)) & (bins - 1);
     }
-    rank_tile(digit, in, items, bins, hist, rank, a.hist + c * bins);
+    rank_tile(digit, in, items, a.digit, hist, rank, a.hist + c * (bins / 2));
     cluster.sync();  // every block's totals
-    uint32_t before = 0, all = 0;
-    if (tid < bins) {
+    uint32_t b0 = 0, b1 = 0, all0 = 0, all1 = 0;  // two digits: before this block, of all
+    if (tid < bins / 2) {
       uint32_t t[kMaxCluster];
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r)
-        t[r] = r < nc ? __ldcg(a.hist + r * bins + tid) : 0;
+        t[r] = r < nc ? __ldcg(a.hist + r * (bins / 2) + tid) : 0;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        all += t[r];
-        before += r < c ? t[r] : 0;
+        all0 += t[r] & 0xffffu;
+        all1 += t[r] >> 16;
+        b0 += r < c ? t[r] & 0xffffu : 0;
+        b1 += r < c ? t[r] >> 16 : 0;
       }
     }
     int sum;
-    const int first = sort_scan((int)all, s_scan, &sum);
-    if (tid < bins) base[tid] = (uint32_t)first + before;
+    const uint32_t first = (uint32_t)sort_scan((int)(all0 + all1), s_scan, &sum);
+    if (tid < bins / 2) {
+      base[2 * tid] = first + b0;
+      base[2 * tid + 1] = first + all0 + b1;
+    }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kSortItems; ++k) {
@@ -599,10 +609,18 @@ __global__ void __launch_bounds__(kSortThreads)
       const uint32_t r = to / (uint32_t)tile;
       cluster.map_shared_rank(pair2, (int)r)[to - r * (uint32_t)tile] = x[k];
     }
+    __syncwarp();
+    if (p + 1 < a.passes) clear_counts(hist, a.digit);
     cluster.sync();  // every pair has arrived
     uint2* t = pair;
     pair = pair2;
     pair2 = t;
+  }
+  uint32_t* out_key = a.key[a.passes & 1] + c * tile;
+  uint32_t* out_val = a.val[a.passes & 1] + c * tile;
+  for (int i = tid; i < n; i += kSortThreads) {
+    out_key[i] = pair[i].x;
+    out_val[i] = pair[i].y;
   }
   // segments: this thread's `items` consecutive sorted positions
   const uint32_t left = c > 0 && n > 0 ? cluster.map_shared_rank(pair, c - 1)[tile - 1].x : 0;
@@ -639,12 +657,8 @@ __global__ void __launch_bounds__(kSortThreads)
   }
   __syncthreads();
   seg += s_before;
-  uint32_t* out_key = a.key[a.passes & 1] + c * tile;
-  uint32_t* out_val = a.val[a.passes & 1] + c * tile;
-  for (int i = tid; i < n; i += kSortThreads) {
-    out_key[i] = pair[i].x;
-    out_val[i] = pair[i].y;
-  }
+  // through the buffer that is free now, so that they are written side by side
+  uint32_t* number = reinterpret_cast<uint32_t*>(pair2);
   for (int k = 0; k < items; ++k) {
     const int i = i0 + k;
     if (i >= n) break;
@@ -655,8 +669,10 @@ __global__ void __launch_bounds__(kSortThreads)
       if (a.row_ids) a.row_ids[seg] = (int64_t)key;
       ++seg;
     }
-    a.rank[c * tile + i] = (uint32_t)(seg - 1);
+    number[i] = (uint32_t)(seg - 1);
   }
+  __syncthreads();
+  for (int i = tid; i < n; i += kSortThreads) a.rank[c * tile + i] = number[i];
 }
 
 // ---------------------------------------------------------------- sums
