@@ -13,7 +13,7 @@
 // positions.  A segment inside one warp's positions is written at once; the
 // parts of a segment that passes a warp's border are joined through shared
 // memory, and the parts of one that passes a block's border through the
-// workspace (at most two partial rows per block), by k_embed_join.
+// workspace (at most two partial rows per block), by the last of its blocks.
 #include <cuda_bf16.h>
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>

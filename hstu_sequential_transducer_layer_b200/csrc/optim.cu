@@ -606,20 +606,28 @@ DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst
   }
 }
 
-// Block b of a row-sparse tensor; false (and the status set) if its row is not
-// one of the table or not above the row before.
-DEVI bool row_block(const StepTensor& q, int64_t b, int* status, BlockAt& at) {
-  const int64_t i = q.row_blocks == 1 ? b : (int64_t)((uint64_t)b / (uint32_t)q.row_blocks);
-  const int j = (int)(b - i * q.row_blocks);
-  const int64_t row = q.row_ids[i], before = i > 0 ? q.row_ids[i - 1] : -1;
-  if (row < 0 || row >= q.rows || before >= row) {
+// A warp's walk over the blocks of a row-sparse tensor: block j of row i of the
+// list, the row's number asked for one block ahead.
+struct RowWalk {
+  int64_t i;
+  int j;
+  int64_t row, before;  // table row, and the one before it in the list
+};
+DEVI void ask_row(const StepTensor& q, RowWalk& w, int64_t rows) {
+  w.row = w.i < rows ? q.row_ids[w.i] : 0;
+  w.before = w.i < rows && w.i > 0 ? q.row_ids[w.i - 1] : -1;
+}
+// Where the block lies; false (and the status set) if its row is not one of the
+// table's or not above the one before.
+DEVI bool row_block(const StepTensor& q, const RowWalk& w, int* status, BlockAt& at) {
+  if (w.row < 0 || w.row >= q.rows || w.before >= w.row) {
     if ((threadIdx.x & 31) == 0) atomicCAS(status, HSTU_OK, HSTU_ERR_BAD_IDS);
     return false;
   }
-  at.g0 = i * q.row_len + j * kBlockElems;
-  at.p0 = row * q.row_len + j * kBlockElems;
-  at.block = row * q.row_blocks + j;
-  at.len = min(kBlockElems, q.row_len - j * kBlockElems);
+  at.g0 = w.i * q.row_len + w.j * kBlockElems;
+  at.p0 = w.row * q.row_len + w.j * kBlockElems;
+  at.block = w.row * q.row_blocks + w.j;
+  at.len = min(kBlockElems, q.row_len - w.j * kBlockElems);
   return true;
 }
 
@@ -715,19 +723,34 @@ __global__ void __launch_bounds__(kThreads, S8 ? 7 : 6)
         step_block_any<S8>(q, at, k, key);
       }
     } else {
-      const int64_t blocks =
-          min(max(*q.n_rows, (int64_t)0), (int64_t)q.max_rows) * q.row_blocks;
-      if (q.row_len % 4) {
-        for (; b < blocks; b += next)
-          if (row_block(q, b, a.status, at)) step_block_any<S8>(q, at, k, key);
-      } else {
-        for (; b < blocks; b += next) {
-          if (!row_block(q, b, a.status, at)) continue;
-          uint8_t* scale = lane < 16 ? q.m_scale : q.v_scale;
-          int bytes = S8 ? scale[at.block] : 0;
-          step_block<S8, FAST, false>(q, at, k, key, 0, bytes);
-          if (S8 && (lane & 15) == 0) scale[at.block] = (uint8_t)bytes;
+      const int64_t rows = min(max(*q.n_rows, (int64_t)0), (int64_t)q.max_rows);
+      const int64_t di = next / q.row_blocks;
+      const int dj = (int)(next - di * q.row_blocks);
+      RowWalk w;
+      w.i = b / q.row_blocks;
+      w.j = (int)(b - w.i * q.row_blocks);
+      ask_row(q, w, rows);
+      while (w.i < rows) {
+        const bool in = row_block(q, w, a.status, at);
+        w.i += di;
+        w.j += dj;
+        if (w.j >= q.row_blocks) {
+          w.j -= q.row_blocks;
+          ++w.i;
         }
+        ask_row(q, w, rows);
+        if (!in) continue;
+        if (q.row_len % 4) {
+          step_block_any<S8>(q, at, k, key);
+          continue;
+        }
+        uint8_t* scale = lane < 16 ? q.m_scale : q.v_scale;
+        int bytes = S8 ? scale[at.block] : 0;
+        if (at.len == kBlockElems)
+          step_block<S8, FAST, true>(q, at, k, key, 0, bytes);
+        else
+          step_block<S8, FAST, false>(q, at, k, key, 0, bytes);
+        if (S8 && (lane & 15) == 0) scale[at.block] = (uint8_t)bytes;
       }
     }
   }
