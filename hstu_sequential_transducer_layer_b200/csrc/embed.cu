@@ -41,6 +41,7 @@ constexpr int kColumns = 256;                      // columns of one block, 8 pe
 
 constexpr int64_t kMaxTokens = 0x7fffffffll - kSortTile;
 constexpr int64_t kMaxRows = 0x7ffffffell;
+constexpr int64_t kMaxStride = (int64_t)1 << 31;
 
 // ---------------------------------------------------------------- elements
 // 8 elements of a row as fp32.  Vector form: the lane's 8 consecutive ones,
@@ -255,12 +256,12 @@ struct SortArgs {
   int64_t* n_unique;       // compact form: their number (else null)
   int32_t* status;
   uint32_t* arrived;       // counters of the sums, cleared here
-  int n_arrived;
+  int64_t n_arrived;
 };
 
 // Clears the sums' counters; block `b` of `n`.
 DEVI void clear_arrived(const SortArgs& a, int b, int n) {
-  for (int i = b * kSortThreads + threadIdx.x; i < a.n_arrived; i += n * kSortThreads)
+  for (int64_t i = b * kSortThreads + threadIdx.x; i < a.n_arrived; i += n * kSortThreads)
     a.arrived[i] = 0;
 }
 
@@ -907,7 +908,8 @@ size_t dsize(int32_t t) { return t == HSTU_FP32 ? 4 : 2; }
 
 struct BwdLayout {
   size_t head, key[2], val[2], hist, bad, heads, sums, rank, seg_start, arrived, part, total;
-  int tiles, passes, digit, runs, ld_part, n_arrived;
+  int tiles, passes, digit, runs, ld_part;
+  int64_t n_arrived;
 };
 
 bool bwd_layout(int64_t T, int64_t R, int32_t d, BwdLayout* L) {
@@ -936,7 +938,7 @@ bool bwd_layout(int64_t T, int64_t R, int32_t d, BwdLayout* L) {
   L->heads = take((size_t)L->tiles * 4);
   L->rank = take((size_t)T * 4);
   L->seg_start = take(((size_t)T + 1) * 4);
-  L->n_arrived = L->runs * (L->ld_part / kColumns);
+  L->n_arrived = (int64_t)L->runs * (L->ld_part / kColumns);
   L->arrived = take((size_t)L->n_arrived * 4);
   L->part = take((size_t)L->runs * 2 * L->ld_part * 4);
   L->total = off;
@@ -1048,7 +1050,9 @@ hstu_status embed_bwd(int64_t T, const int64_t* ids, const void* dY, int32_t dy_
                       int64_t ld_out, void* ws, size_t ws_bytes, cudaStream_t s) {
   BwdLayout L;
   if (!bwd_layout(T, R, d, &L)) return HSTU_ERR_INVALID_ARG;
-  if (!dtype_ok(dy_dt) || !dtype_ok(out_dt) || ld_dy < d || ld_out < d) return HSTU_ERR_INVALID_ARG;
+  if (!dtype_ok(dy_dt) || !dtype_ok(out_dt) || ld_dy < d || ld_out < d || ld_dy > kMaxStride ||
+      ld_out > kMaxStride)
+    return HSTU_ERR_INVALID_ARG;
   if (accumulate != 0 && accumulate != 1) return HSTU_ERR_INVALID_ARG;
   if (!(scale - scale == 0.f)) return HSTU_ERR_INVALID_ARG;  // NaN or infinite
   if (T > 0 && (!ids || !dY || !out)) return HSTU_ERR_INVALID_ARG;
@@ -1167,7 +1171,8 @@ hstu_status hstu_embed_fwd(int64_t n_tokens, const int64_t* ids, const void* tab
   using namespace hstu;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n_tokens < 0 || n_tokens > kMaxTokens || n_rows < 1 || n_rows > kMaxRows || d < 1 ||
-      d > (1 << 20) || ld_table < d || ld_out < d || !dtype_ok(table_dtype) || !dtype_ok(out_dtype))
+      d > (1 << 20) || ld_table < d || ld_out < d || ld_table > kMaxStride || ld_out > kMaxStride ||
+      !dtype_ok(table_dtype) || !dtype_ok(out_dtype))
     return HSTU_ERR_INVALID_ARG;
   if (!(scale - scale == 0.f)) return HSTU_ERR_INVALID_ARG;  // NaN or infinite
   if (n_tokens > 0 && (!ids || !table || !out)) return HSTU_ERR_INVALID_ARG;

@@ -81,7 +81,8 @@ class HSTUTrainer:
         stack's output.  `ids` (with a table): the table row of each row of X,
         which was looked up with the factor `embed_scale`.  `lr`: this step's
         rate (default: the constructor's).  Returns dX; `norm` holds the
-        gradient norm and the clip factor."""
+        gradient norm and the clip factor.  A step whose gradients are not all
+        finite (clip factor NaN) changes nothing, but is counted in `steps`."""
         dX, _ = self.runner.stack_bwd(offsets, X, timestamps, dY, max_len, grads=self.grads,
                                       stream=stream)
         if (ids is None) != (self.table is None):

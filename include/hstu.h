@@ -396,11 +396,12 @@ hstu_status hstu_sl_embed_ids(int64_t B, int64_t raw_total, int64_t max_raw_len,
 /* Embedding lookup with scaling: out[t, :] = scale * table[ids[t], :], the
  * product in fp32 and rounded once to out_dtype.
  *   ids     device int64 [n_tokens]; a token whose id is pad_id gets a zero
- *           row (pass -1 for no padding; any id may be the padding's)
+ *           row.  pad_id may be a row of the table or any number outside it
+ *           (the binding's default is -1: hstu_sl_embed_ids's mark of a bad id)
  *   table   device [n_rows, d] of table_dtype, ld_table elements apart
  *   out     device [n_tokens, d] of out_dtype, ld_out elements apart; the gap
  *           behind each row is left as it was
- * Any d up to 2^20 and any strides; rows are moved 16 bytes at a time where d
+ * Any d up to 2^20 and any strides up to 2^31; rows are moved 16 bytes at a time where d
  * and both strides are multiples of 8, else element by element.  n_tokens and
  * n_rows below 2^31 - 8192.  An id outside the table that is not pad_id gets a
  * zero row and sets HSTU_ERR_BAD_IDS in the workspace's status word
@@ -477,7 +478,8 @@ typedef struct {
  * the factor that clips it, min(1, max_norm / norm), or NaN when the norm is
  * not finite; out: device fp32 [2], 16-byte aligned.  Only the gradient's
  * fields of each tensor are read (n, grad, grad_dtype, and for a row-sparse
- * one row_len, max_rows, n_rows).  max_norm > 0 (infinity: never clips).  At
+ * one row_len, max_rows, n_rows; a row count outside [0, max_rows] is cut to
+ * it).  max_norm > 0 (infinity: never clips).  At
  * most HSTU_MAX_TENSORS tensors (host array).  Deterministic on one device. */
 size_t hstu_grad_norm_workspace_size(void);
 hstu_status hstu_grad_norm(const hstu_adamw_tensor* tensors, int32_t n_tensors, double max_norm,

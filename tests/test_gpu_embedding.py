@@ -160,6 +160,37 @@ def test_gradient(T, R, d, kind, compact):
         np.testing.assert_array_equal(rows, np.flatnonzero(n))
 
 
+@pytest.mark.parametrize("compact", [False, True])
+@pytest.mark.parametrize("T,R,d,kind", [
+    (131072, 1000, 8, "few"), (131073, 3000000, 8, "few"), (140000, 2, 50, "few"),
+    (262145, 70000, 16, "each"), (300001, 1, 8, "one"), (400000, 1 << 25, 8, "uniform")])
+def test_gradient_of_many_tokens(T, R, d, kind, compact):
+    """Around and beyond the 131,072 tokens that one cluster of blocks sorts."""
+    import torch
+    if not compact and R * d > 1 << 26:
+        R = 100000
+    ids = _tokens(T, R, T, kind)
+    dY = torch.randn(T, d, device="cuda", generator=torch.Generator("cuda").manual_seed(T)) \
+        .to(torch.bfloat16)
+    pad = int(ids[7]) if kind == "few" else -1
+    st, got, rows, _ = _gradient(ids, dY, R, 2.0, pad, compact=compact)
+    assert st == 0
+    keep = ids != pad
+    y = 2.0 * dY.double().cpu().numpy()[keep]
+    touched, at = np.unique(ids[keep], return_inverse=True)
+    ref, mag, n = np.zeros((len(touched), d)), np.zeros((len(touched), d)), np.bincount(at)
+    np.add.at(ref, at, y)
+    np.add.at(mag, at, np.abs(y))
+    tol = (n[:, None] + 2) * 2.0 ** -24 * mag + 2.0 ** -24 * np.abs(ref)
+    assert (np.abs(got[touched] - ref) <= tol).all()
+    assert not np.delete(got, touched, axis=0).any()
+    if compact:
+        np.testing.assert_array_equal(rows, touched)
+    if T % 2:
+        ids[T // 3] = R + 5
+        assert _gradient(ids, dY, R, 2.0, pad, compact=compact)[0] == BAD_IDS
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("d,ld", [(40, 40), (40, 48), (41, 43), (512, 512)])
 def test_gradient_output_types_and_accumulation(out, d, ld):

@@ -239,6 +239,47 @@ def test_many_tensors():
     assert H.hstu_read_status(ws) == 0
 
 
+@pytest.mark.parametrize("tail", [0, 5, 256 * 3, 256 * 7 + 255])
+def test_large_tensors(tail):
+    """Lists large enough for a warp to take several consecutive blocks at a
+    time: blocks at the start, at the end (whole and not) and all over a large
+    8-bit tensor, with small tensors of either width around it."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    n = 20_000_000 - 20_000_000 % 2048 + tail
+    ts = [_make(700, "bf16", "f32", True, 8, 1), _make(n, "bf16", "f32", True, 8, 2),
+          _make(5000, "f32", "f32", False, 32, 3), _make(2000, "bf16", "bf16", False, 8, 4)]
+    old = [_copy(t) for t in ts]
+    ws = _ws(256)
+    H.hstu_adamw_step(H.AdamWTensors(ts), ws, step=9, seed=8, **HYPER)
+    assert H.hstu_read_status(ws) == 0
+    for i in (0, 2, 3):
+        _check(old[i], ts[i], 9, 1.0, i, 8, name="f32" if i == 2 else "bf16")
+    nb = -(-n // 256)
+    rng = np.random.default_rng(tail)
+    pick = np.unique(np.concatenate([np.arange(40), np.arange(nb - 40, nb), rng.integers(0, nb, 2000)]))
+    at = (pick[:, None] * 256 + np.arange(256)).ravel()
+    live = at < n
+    idx = torch.from_numpy(np.minimum(at, n - 1)).cuda()
+
+    def cut(t, k):
+        x = t[k].view(torch.uint8)[idx] if k in ("m", "v") else t[k][idx]
+        x = x.cpu().numpy() if k in ("m", "v") else _np(x)
+        return np.where(live, x, 0).reshape(-1, 256)
+    o, t = old[1], ts[1]
+    sc = {k: o[k].cpu().numpy()[pick] for k in ("m_scale", "v_scale")}
+    cm, sm, cr, sr = TR.adamw_step_8bit(cut(o, "m"), sc["m_scale"], cut(o, "v"), sc["v_scale"],
+                                        cut(o, "grad").astype(np.float32), 8, 9, 1, pick,
+                                        HYPER["beta1"], HYPER["beta2"])
+    np.testing.assert_array_equal(cut(t, "m").ravel()[live], cm.ravel()[live])
+    np.testing.assert_array_equal(cut(t, "v").ravel()[live], cr.ravel()[live])
+    np.testing.assert_array_equal(t["m_scale"].cpu().numpy()[pick], sm)
+    np.testing.assert_array_equal(t["v_scale"].cpu().numpy()[pick], sr)
+    m, r = TR.decode(cut(o, "m"), sc["m_scale"]), TR.decode(cut(o, "v"), sc["v_scale"])
+    rp, _, _, dp, _, _ = _bounds(cut(o, "master"), cut(o, "grad"), m, r ** 2, 9, 0.0, 1.0)
+    assert (np.abs(cut(t, "master") - rp) <= dp).all()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("R,d,U,cap", [(1, 1, 1, 1), (9, 50, 0, 4), (9, 50, 9, 9), (300, 257, 77, 90),
                                        (300, 256, 77, 300), (1000, 8, 400, 401), (64, 1024, 33, 50)])
@@ -412,6 +453,26 @@ def test_captured_step_reads_step_and_rate_from_the_device():
             for q in a:
                 assert torch.equal(a[q], b[q]), q
     del graph
+
+
+def test_lists_on_two_streams_at_once():
+    """Two lists, each with its own workspace, on two streams."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    ts = [[_make(300_000, "bf16", "f32", True, b, b)] for b in (8, 32)]
+    old = [[_copy(t[0])] for t in ts]
+    lst, ws = [H.AdamWTensors(t) for t in ts], [_ws(256), _ws(256)]
+    out, nws = [torch.zeros(2, device="cuda") for _ in ts], \
+        [_ws(H.hstu_grad_norm_workspace_size()) for _ in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    torch.cuda.synchronize()
+    for k in range(2):
+        H.hstu_grad_norm(lst[k], 1.0, out[k], nws[k], stream=streams[k])
+        H.hstu_adamw_step(lst[k], ws[k], step=1, grad_scale=out[k][1:], seed=2, stream=streams[k],
+                          **HYPER)
+    torch.cuda.synchronize()
+    for k in range(2):
+        _check(old[k][0], ts[k][0], 1, float(out[k][1]), 0, 2)
 
 
 def test_offsets_past_32_bits():

@@ -119,6 +119,7 @@ def test_embedding_refusals():
         k.get("wsb", 256), None)
     for bad in (dict(T=-1), dict(T=1 << 31), dict(R=0), dict(R=1 << 31), dict(d=0), dict(ldt=63),
                 dict(ldo=63), dict(dt=3), dict(odt=-1), dict(s=math.nan), dict(s=math.inf),
+                dict(ldt=1 << 32), dict(ldo=1 << 32),
                 dict(ids=None), dict(tab=None), dict(out=None), dict(tab=0x2008), dict(out=0x3002),
                 dict(ids=0x1008)):
         assert fwd(**bad) == 1, bad
@@ -172,7 +173,7 @@ def test_optimizer_refusals():
             setattr(a, f, x)
         return L.hstu_adamw_step(ctypes.byref(a), ctypes.byref(t or _tensor()), n, w, wb, None)
 
-    for bad in (dict(step=0), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(eps=0.0),
+    for bad in (dict(step=0), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(eps=0.0), dict(eps=1e-39),
                 dict(eps=math.nan), dict(lr=math.inf), dict(beta2=math.nan)):
         assert step(**bad) == 1, bad
     rows = dict(row_ids=0x5000, n_rows=0x6000, row_len=64, max_rows=10)
