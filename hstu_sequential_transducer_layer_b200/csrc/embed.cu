@@ -9,7 +9,7 @@
 // A user whose tokens are half actions gives segments of very different
 // length (an action row holds thousands of tokens, most content rows one or
 // two), so the sum is cut by sorted position, not by row: a block takes
-// kRun = 128 consecutive positions and 256 columns, each of its 8 warps 16
+// kRun = 96 consecutive positions and 256 columns, each of its 6 warps 16
 // positions.  A segment inside one warp's positions is written at once; the
 // parts of a segment that passes a warp's border are joined through shared
 // memory, and the parts of one that passes a block's border through the
@@ -34,7 +34,7 @@ constexpr int kMaxCluster = 16;
 constexpr int kDigitBits = 10;  // at most; bins of one pass
 constexpr int kMaxBins = 1 << kDigitBits;
 
-constexpr int kRunWarps = 8;
+constexpr int kRunWarps = 6;
 constexpr int kRunTokens = 16;                     // sorted positions of one warp
 constexpr int kRun = kRunWarps * kRunTokens;       // of one block
 constexpr int kColumns = 256;                      // columns of one block, 8 per lane
@@ -757,7 +757,7 @@ struct Chain {
 // lane 17 the key behind; one ballot tells where segments start, so the loop
 // over the tokens has no exchange but the token's number.
 template <int DT, bool VEC, bool PLAIN>
-__global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const SumArgs a) {
+__global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const SumArgs a) {
   __shared__ float s_pre[kRunWarps][kColumns], s_post[kRunWarps][kColumns];
   __shared__ int s_flags[kRunWarps];  // 1: pre holds a part, 2: it goes on past this warp
   __shared__ Chain s_chain[2];        // of the run's first position, and of its last one
@@ -788,7 +788,10 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
   int flags = 0;
-  constexpr int kBatch = DT == HSTU_FP32 ? 2 : 4;  // 8 would spill at 64 registers: 3 us of 49 slower
+  // 8 rows of 16 bits in flight would spill at 64 registers (49 us of the touched rows of
+  // 38,070 x 1024 against 46); 6 warps a block, 6 blocks a SM: 56 registers and nothing spilled
+  // (dense gradient of 65,536 x 512: 69 us; 8 warps, 4 blocks: 72)
+  constexpr int kBatch = DT == HSTU_FP32 ? 2 : 4;
   for (int i0 = 0; i0 < n; i0 += kBatch) {
     Raw8<DT> r[VEC ? kBatch : 1];
     float one[VEC ? 1 : kBatch][8];
@@ -802,7 +805,8 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 4 : 2) k_embed_sum(const
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int c = 32 * j + lane;
-          one[u][j] = i0 + u < n && c0 + c < a.d ? load1<DT>(a.dY, row + c) : 0.f;
+          one[u][j] = 0.f;
+          if (c0 + 32 * j < a.d && i0 + u < n && c0 + c < a.d) one[u][j] = load1<DT>(a.dY, row + c);
         }
       }
     }
