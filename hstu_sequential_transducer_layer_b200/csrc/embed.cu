@@ -148,9 +148,11 @@ struct LookupArgs {
 constexpr int kLookupUnroll = 4;
 constexpr int64_t kCheckMax = 65536;
 
-// Y[t] = scale * E[ids[t]].  Bandwidth-bound; a thread keeps one column
-// group of 8 elements (1 where a row is not a multiple of 8) and walks the
-// tokens, 4 loads in flight, so that no index is divided inside the loop.
+// Y[t] = scale * E[ids[t]].  Bandwidth-bound (19.7 us for 38,070 x 1024 bf16:
+// 78 MB written and the touched rows read, at 4.6 TB/s; setting 78 MB to zero
+// takes 20.7); a thread keeps one column group of 8 elements (1 where a row is
+// not a multiple of 8) and walks the tokens, 4 loads in flight, so that no index
+// is divided inside the loop.
 // Both types are compiled in: with a branch on the output's type per store the
 // kernel was bound by instructions (12.5 per element).  A dropped token's
 // loads are replaced by zeros.
@@ -332,10 +334,11 @@ __global__ void k_sort_scan(const SortArgs a, int pass) {
 // Ranks a tile's items among those of the same digit, in tile order: each
 // warp counts its own 32 * items consecutive items (equal digits of one
 // 32-item step found by match: 850 cycles a step of 32 warps, against 1300 with
-// one ballot per bit), then the warps' counts are summed up per digit.  On return hist[w][b] is the number of items of digit b in warps
-// before w, rank[k] this thread's item's number inside its warp, and total[b]
-// (if given) the tile's number of items of digits 2 b (low half) and 2 b + 1.
-// Every warp's counts (its row of hist) must be zero before.
+// one ballot per bit), then the warps' counts are summed up per digit.  Every
+// warp's counts (its row of hist, clear_counts) must be zero before.  On return
+// hist[w][b] is the number of items of digit b in warps before w, rank[k] this
+// thread's item's number inside its warp, and total[b] (if given) the tile's
+// number of items of digits 2 b (low half) and 2 b + 1.
 DEVI void clear_counts(uint16_t* hist, int bits) {
   const int row = 2 << bits;  // bytes
   uint8_t* mine = reinterpret_cast<uint8_t*>(hist) + (threadIdx.x >> 5) * row;
@@ -473,15 +476,21 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_segments(const SortArgs a
 // ---------------------------------------------------------------- one-launch sort
 // Up to kClusterTokens tokens are sorted by one cluster of up to 16 blocks,
 // each holding its tile of (key, token) pairs in shared memory: a pass ranks
-// the tile, adds up the blocks' digit counts and writes every pair into the shared memory of the block that its
-// new position falls to.  The blocks' digit counts go through global memory: 16
-// blocks reading 1024 counts of each other are 64 KB per block, which took 10,300
-// cycles a pass as shared-memory reads across the cluster.  The barriers of a
-// pass are the cluster's own (they order global memory too), so the whole sort
-// with the segments' numbers is one launch.  The launch's other
-// clusters clear the dense gradient meanwhile (if there is one to clear): the
-// sort is bound by its barriers and leaves the memory idle.  Where that leaves
-// room in the L2 cache they ask it for dY, which the sums read next.
+// the tile, adds up the blocks' digit counts and writes every pair into the
+// shared memory of the block that its new position falls to.  The blocks'
+// digit counts go through global memory: 16 blocks reading 1024 counts of each
+// other are 64 KB per block, which took 10,300 cycles a pass as shared-memory
+// reads across the cluster and takes 2,400 through L2.  The barriers of a pass
+// are the cluster's own (they order global memory too), so the whole sort with
+// the segments' numbers is one launch, where the kernels above are 3 per pass
+// and 2 more.  It is bound by latency: 19 us for 38,070 tokens of a table of
+// 1M rows (two passes of 10 bits, 5 us each), 27 for 82,351, 8 for 3,271 of 8
+// rows, against 80 with the kernels above.
+//
+// The launch's other clusters clear the dense gradient meanwhile (if there is
+// one to clear): the sort leaves the memory idle.  Where that leaves room in
+// the L2 cache they ask it for dY, which the sums read next (touched rows of
+// 38,070 x 1024: 50 -> 46 us).
 constexpr int64_t kClusterTokens = (int64_t)kMaxCluster * kSortTile;
 
 struct FillArgs {
@@ -492,9 +501,12 @@ struct FillArgs {
   int64_t ask_bytes;   // a multiple of 16
 };
 
+// Asks the L2 cache for dY while the tokens are sorted: at most what leaves
+// room in its 126 MB, nothing where it is too little to be worth the extra
+// cluster, and nothing beside a larger gradient to clear, which would push it
+// out again.  (16 KB per request instead of 4 took twice as long.)
 constexpr int64_t kAskMost = (int64_t)96 << 20, kAskLeast = (int64_t)4 << 20,
                   kAskFill = (int64_t)32 << 20;
-// Asks the L2 cache for dY while the tokens are sorted.
 constexpr int kAskChunk = 4096;
 DEVI void ask_l2(const FillArgs& f, int64_t block, int64_t blocks) {
   for (int64_t o = (block * kSortThreads + threadIdx.x) * kAskChunk; o < f.ask_bytes;
@@ -638,8 +650,9 @@ __global__ void __launch_bounds__(kSortThreads)
   int all;
   int seg = sort_scan(count, s_scan, &all) & 0xffff;
   const int any_bad = __syncthreads_or(bad);
-  if (tid == 0) *reinterpret_cast<int4*>(a.sums + 4 * c) = make_int4(any_bad, all & 0xffff, all >> 16, 0);
-  cluster.sync();  // the blocks' sums; also the last access to another block's shared memory is done
+  if (tid == 0)
+    *reinterpret_cast<int4*>(a.sums + 4 * c) = make_int4(any_bad, all & 0xffff, all >> 16, 0);
+  cluster.sync();  // the blocks' sums; and no block's shared memory is read by another any more
   if (warp == 0) {
     const int4 o = lane < nc ? __ldcg(reinterpret_cast<const int4*>(a.sums) + lane)
                              : make_int4(0, 0, 0, 0);
@@ -693,13 +706,8 @@ struct SumArgs {
   int d, ld_part, out_dt, compact, accumulate;
 };
 
-// Column (vector form: first of 8) of this lane, and the elements' stride.
-template <bool VEC>
-DEVI int lane_col(int lane, int j) {
-  return VEC ? 8 * lane + j : 32 * j + lane;
-}
-
-// PLAIN: fp32, not accumulated.
+// Writes (or adds into) a row of the gradient, this lane's 8 columns: 8 lane +
+// 0 .. 7 (VEC), or lane + 32 j.  PLAIN: fp32, not accumulated.
 template <bool VEC, bool PLAIN>
 DEVI void write_row(const SumArgs& a, uint32_t key, uint32_t rank, int c0, int lane,
                     const float (&acc)[8]) {

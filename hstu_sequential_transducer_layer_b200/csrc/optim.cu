@@ -326,11 +326,6 @@ DEVI void widen4(int dtype, const uint4& r, float (&f)[4]) {
 }
 DEVI uint32_t bits2(const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); }
 DEVI uint32_t bits2(const __half2& x) { return *reinterpret_cast<const uint32_t*>(&x); }
-// fp16 pair, saturating at +-65504 as hstu_bf16_to_f16 does.
-DEVI uint32_t half2_sat(float2 x) {
-  return bits2(__hmin2(__hmax2(__floats2half2_rn(x.x, x.y), __float2half2_rn(-65504.f)),
-                       __float2half2_rn(65504.f)));
-}
 // What storing x in `dtype` leaves of it.
 DEVI float rounded(int dtype, float x) {
   return dtype == HSTU_FP32   ? x
@@ -407,7 +402,7 @@ DEVI void store_param(const StepTensor& q, int64_t at, const float (&p)[4]) {
     *reinterpret_cast<uint2*>(static_cast<__half*>(q.param) + at) = make_uint2(bits2(s), bits2(t));
     x = __half22float2(s), y = __half22float2(t);
   }
-  if (q.copy) *reinterpret_cast<uint2*>(q.copy + at) = make_uint2(half2_sat(x), half2_sat(y));
+  if (q.copy) *reinterpret_cast<uint2*>(q.copy + at) = make_uint2(pack_f16x2_sat(x.x, x.y), pack_f16x2_sat(y.x, y.y));
 }
 
 // The step of one block whose length is a multiple of 4 and whose rows are
@@ -576,7 +571,7 @@ DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst
     store_elem(q.param_dtype, q.param, x, p);
     if (q.copy) {
       const float y = rounded(q.param_dtype, p);
-      q.copy[x] = __ushort_as_half((unsigned short)half2_sat(make_float2(y, y)));
+      q.copy[x] = __ushort_as_half((unsigned short)pack_f16x2_sat(y, y));
     }
     const uint32_t a = abs_bits(m[i]), b = abs_bits(root[i]);
     top_m = max(top_m, a < kInfBits ? a : 0);
@@ -642,11 +637,12 @@ DEVI bool row_block(const StepTensor& q, const RowWalk& w, int* status, BlockAt&
 // SMs, which cost 20 to 45 us of 184 on 42M parameters.
 //
 // Thread blocks of 128 threads per SM, measured on 42M parameters: fp32 states
-// 6 resident (80 registers), 16 launched (218 us; 8 resident at 64 registers
-// 235, 16 resident waves of one launch 236: the hardware's handing out of
-// thread blocks evens out what a fixed share does not); 8-bit states, bound by
-// instructions as much as by memory, 7 resident and launched (160 us; 8
-// resident at 64 registers, which spill, 171; 6 164).
+// 6 resident (80 registers) and 16 launched (218 us, 6.2 TB/s; 8 resident at 64
+// registers 235; no more launched than resident 228: the hardware's handing
+// out of thread blocks evens out what a fixed share does not); 8-bit states,
+// bound by instructions (about 100 per element) as much as by memory, 7
+// resident and launched (160 us, 5.3 TB/s; 8 resident at 64 registers, which
+// spill, 171; 6 resident 164).
 template <bool S8, bool FAST, int N>
 __global__ void __launch_bounds__(kThreads, S8 ? 7 : 6)
     k_adamw(const __grid_constant__ StepArgs<N> a) {

@@ -392,6 +392,26 @@ def test_not_finite_gradients_stay_in_their_element():
             assert (t["m"][~keep] & 0x7F == 0x7F).all() and (t["v"][~keep] == 0x7F).all()
 
 
+def test_fp16_copy_is_what_the_conversion_gives():
+    """The copy of each new bf16 parameter, bit for bit as hstu_bf16_to_f16:
+    values beyond fp16's range, subnormals, zeros, NaN; whole blocks and the
+    end of a tensor."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    n = 1000
+    p = torch.exp(torch.linspace(-40, 40, n, device="cuda")) * \
+        torch.tensor([1.0, -1.0], device="cuda").repeat(n // 2)
+    p[3], p[4], p[998] = math.nan, 0.0, math.nan
+    z = lambda: torch.zeros(n, device="cuda")  # noqa: E731
+    t = dict(param=p.bfloat16(), master=p.clone(), grad=z(), m=z(), v=z(),
+             copy_f16=torch.zeros(n, dtype=torch.float16, device="cuda"))
+    H.hstu_adamw_step(H.AdamWTensors([t]), _ws(256), step=1, **HYPER)
+    want = torch.zeros_like(t["copy_f16"])
+    H.hstu_bf16_to_f16(t["param"], want)
+    assert torch.equal(t["copy_f16"].view(torch.int16), want.view(torch.int16))
+    assert torch.isnan(want[3]) and torch.isnan(want[998]) and float(want[n - 4]) == 65504.0
+
+
 def test_small_second_moments_keep_moving():
     """v moves by 1e-3 of itself per step, far less than a code step s <= 2^-3 of
     its root: under rounding to nearest it would stand still.  100 steps with
