@@ -772,7 +772,6 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b0 = blockIdx.x * kRun, c0 = blockIdx.y * kColumns;
-  if (threadIdx.x < 2) s_chain[threadIdx.x].start = -1;
   grid_dep_wait();
   const int pos = b0 + warp * kRunTokens + lane - 1;
   const bool mine = lane >= 1 && lane <= kRunTokens && pos < a.T;
@@ -784,14 +783,14 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const
   const uint32_t last_key = __shfl_sync(0xffffffffu, key, n);
   const bool on = n > 0 && __shfl_sync(0xffffffffu, key, n + 1) == last_key;  // behind this warp
   bool open = n > 0 && !(heads & 1);  // the running segment began before this warp's positions
-  // the segments at the run's borders: lanes 0 and 1 read where they start and end
-  const int border = warp == 0 && open ? 0 : on && b0 + kRun == pos - lane + 1 + n ? 1 : -1;
-  int bound = 0;
-  uint32_t border_seg = 0;
-  if (border >= 0) {
-    border_seg = __shfl_sync(0xffffffffu, rank, border == 0 ? 1 : n);
-    if (lane < 2) bound = (int)a.seg_start[border_seg + lane];
-  }
+  const uint32_t last_rank = __shfl_sync(0xffffffffu, rank, n);
+  // the segments at the run's borders, which its first and its last warp see: lanes 0 and 1 read
+  // where they start and end
+  const bool edge = warp == 0 || warp == kRunWarps - 1;
+  const bool chained = warp == 0 ? open : on && n == kRunTokens;
+  const uint32_t edge_seg = warp == 0 ? __shfl_sync(0xffffffffu, rank, 1) : last_rank;
+  int bound = -1;
+  if (edge && chained && lane < 2) bound = (int)a.seg_start[edge_seg + lane];
   float acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
@@ -839,7 +838,6 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const
       for (int j = 0; j < 8; ++j) acc[j] += VEC ? x[j] : one[u][j];
     }
   }
-  const uint32_t last_rank = __shfl_sync(0xffffffffu, rank, n);
   bool post = false;
   if (n > 0) {
     if (open) {
@@ -853,11 +851,12 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const
     }
   }
   if (lane == 0) s_flags[warp] = flags;
-  if (border >= 0) {
+  if (edge) {
     const int end = __shfl_sync(0xffffffffu, bound, 1);
     // (a segment that fills the run is the first border's; its key is also lane 0's)
-    if (lane == 0 && (border == 0 || bound >= b0))
-      s_chain[border] = Chain{border == 0 ? key : last_key, border_seg, bound, end};
+    if (lane == 0)
+      s_chain[warp != 0] = Chain{warp == 0 ? key : last_key, edge_seg,
+                                 warp == 0 || bound >= b0 ? bound : -1, end};
   }
   __syncthreads();
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.ld_part + c0;
