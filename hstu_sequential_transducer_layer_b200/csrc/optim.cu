@@ -311,6 +311,10 @@ DEVI uint4 raw4(bool wide, const uint8_t* p, int e) {
   const uint2 w = *reinterpret_cast<const uint2*>(p + 2 * e);
   return make_uint4(w.x, w.y, 0, 0);
 }
+DEVI uint4 wide2(const uint4* p, int i) {
+  const uint2 w = reinterpret_cast<const uint2*>(p)[i];
+  return make_uint4(w.x, w.y, 0, 0);
+}
 DEVI void widen4(int dtype, const uint4& r, float (&f)[4]) {
   if (dtype == HSTU_FP32) {
     f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y);
@@ -405,15 +409,46 @@ DEVI void store_param(const StepTensor& q, int64_t at, const float (&p)[4]) {
   if (q.copy) *reinterpret_cast<uint2*>(q.copy + at) = make_uint2(pack_f16x2_sat(x.x, x.y), pack_f16x2_sat(y.x, y.y));
 }
 
+// 8-bit states: a whole block of 256 elements as it lies in memory, copied into
+// shared memory one block ahead of the arithmetic (two stages per warp).  The
+// arithmetic is long enough that a warp's loads have to be in flight
+// meanwhile, and has no registers to hold them: 160 -> 146 us for 42M
+// parameters.  (fp32 states: 224 us against 218 without it.)
+struct Stage {
+  uint4 g[64], p[64], m[16], v[16];  // 16-bit gradients and parameters: half
+};
+DEVI void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+               : "memory");
+}
+DEVI void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All copies but those of the last commit have arrived.
+DEVI void copy_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+template <bool FAST>
+DEVI void stage_block(const StepTensor& q, const BlockAt& at, Stage& s) {
+  const int lane = threadIdx.x & 31;
+  const bool gw = grad_wide<FAST>(q), pw = param_wide<FAST>(q);
+  const uint8_t* gp = static_cast<const uint8_t*>(q.grad) + (at.g0 << (gw ? 2 : 1)) + 16 * lane;
+  const uint8_t* wp = static_cast<const uint8_t*>(q.master ? q.master : q.param) +
+                      (at.p0 << (pw ? 2 : 1)) + 16 * lane;
+  const uint8_t* cp = static_cast<const uint8_t*>(lane < 16 ? q.m : q.v) + at.p0 + 16 * (lane & 15);
+  copy16(&s.g[lane], gp);
+  if (gw) copy16(&s.g[32 + lane], gp + 512);
+  copy16(&s.p[lane], wp);
+  if (pw) copy16(&s.p[32 + lane], wp + 512);
+  copy16((lane < 16 ? s.m : s.v) + (lane & 15), cp);
+}
+
 // The step of one block whose length is a multiple of 4 and whose rows are
-// 16-byte aligned.  WHOLE: 256 elements.  Lane l holds elements 4 l + 128 j +
+// 16-byte aligned.  WHOLE: 256 elements; with 8-bit states staged.  Lane l holds elements 4 l + 128 j +
 // (0..3), j = 0, 1, so every access of a warp is to consecutive addresses;
 // all of a lane's loads are issued before the first one is used.  8-bit
 // states: the block's scale bytes are `bytes` of lanes u (m) and 16 + u (v), and
 // are replaced by the new ones.
 template <bool S8, bool FAST, bool WHOLE>
 DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k, uint64_t key,
-                     int u, int& bytes) {
+                     int u, int& bytes, const Stage* st) {
   const int lane = threadIdx.x & 31;
   const bool gw = grad_wide<FAST>(q), pw = param_wide<FAST>(q);
   const uint8_t* gp = static_cast<const uint8_t*>(q.grad) + (at.g0 << (gw ? 2 : 1));
@@ -424,7 +459,14 @@ DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k,
   uint4 gr[2], pr[2], mr[2], vr[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int e = 4 * lane + 128 * j;
+    const int e = 4 * lane + 128 * j, x = lane + 32 * j;
+    if (S8 && WHOLE) {
+      gr[j] = gw ? st->g[x] : wide2(st->g, x);
+      pr[j] = pw ? st->p[x] : wide2(st->p, x);
+      mr[j].x = reinterpret_cast<const uint32_t*>(st->m)[x];
+      vr[j].x = reinterpret_cast<const uint32_t*>(st->v)[x];
+      continue;
+    }
     if (!WHOLE && e >= at.len) {
       gr[j] = pr[j] = mr[j] = vr[j] = make_uint4(0, 0, 0, 0);
       continue;
@@ -604,26 +646,34 @@ DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst
 // A warp's walk over the blocks of a row-sparse tensor: block j of row i of the
 // list, the row's number asked for one block ahead.
 struct RowWalk {
-  int64_t i;
-  int j;
+  int64_t i, di, rows;
+  int j, dj;
   int64_t row, before;  // table row, and the one before it in the list
 };
-DEVI void ask_row(const StepTensor& q, RowWalk& w, int64_t rows) {
-  w.row = w.i < rows ? q.row_ids[w.i] : 0;
-  w.before = w.i < rows && w.i > 0 ? q.row_ids[w.i - 1] : -1;
+DEVI void ask_row(const StepTensor& q, RowWalk& w) {
+  w.row = w.i < w.rows ? q.row_ids[w.i] : 0;
+  w.before = w.i < w.rows && w.i > 0 ? q.row_ids[w.i - 1] : -1;
 }
-// Where the block lies; false (and the status set) if its row is not one of the
-// table's or not above the one before.
-DEVI bool row_block(const StepTensor& q, const RowWalk& w, int* status, BlockAt& at) {
-  if (w.row < 0 || w.row >= q.rows || w.before >= w.row) {
+// The next block whose row is one of the table's and above the one before (the
+// status is set for any other); false at the end.
+DEVI bool next_block(const StepTensor& q, RowWalk& w, int* status, BlockAt& at) {
+  while (w.i < w.rows) {
+    const bool ok = w.row >= 0 && w.row < q.rows && w.before < w.row;
+    at.g0 = w.i * q.row_len + w.j * kBlockElems;
+    at.p0 = w.row * q.row_len + w.j * kBlockElems;
+    at.block = w.row * q.row_blocks + w.j;
+    at.len = min(kBlockElems, q.row_len - w.j * kBlockElems);
+    w.i += w.di;
+    w.j += w.dj;
+    if (w.j >= q.row_blocks) {
+      w.j -= q.row_blocks;
+      ++w.i;
+    }
+    ask_row(q, w);
+    if (ok) return true;
     if ((threadIdx.x & 31) == 0) atomicCAS(status, HSTU_OK, HSTU_ERR_BAD_IDS);
-    return false;
   }
-  at.g0 = w.i * q.row_len + w.j * kBlockElems;
-  at.p0 = w.row * q.row_len + w.j * kBlockElems;
-  at.block = w.row * q.row_blocks + w.j;
-  at.len = min(kBlockElems, q.row_len - w.j * kBlockElems);
-  return true;
+  return false;
 }
 
 // One step of every tensor of the list whose states have this width and whose
@@ -631,7 +681,7 @@ DEVI bool row_block(const StepTensor& q, const RowWalk& w, int* status, BlockAt&
 // per element the gradient, the states and the (master) parameter are read
 // once and the results written once.
 //
-// 8-bit states: a warp takes 8 consecutive blocks of a large dense tensor at a
+// 8-bit states: a warp takes 4 consecutive blocks of a large dense tensor at a
 // time and reads and writes their scale bytes together.  One block at a time,
 // the bytes of a 32-byte sector were read and written by 32 warps on several
 // SMs, which cost 20 to 45 us of 184 on 42M parameters.
@@ -640,12 +690,12 @@ DEVI bool row_block(const StepTensor& q, const RowWalk& w, int* status, BlockAt&
 // 6 resident (80 registers) and 16 launched (218 us, 6.2 TB/s; 8 resident at 64
 // registers 235; no more launched than resident 228: the hardware's handing
 // out of thread blocks evens out what a fixed share does not); 8-bit states,
-// bound by instructions (about 100 per element) as much as by memory, 7
-// resident and launched (160 us, 5.3 TB/s; 8 resident at 64 registers, which
-// spill, 171; 6 resident 164).
+// bound by instructions (about 95 per element) as much as by memory, 5
+// resident and launched (146 us, 5.8 TB/s; 7, which spill, 166; 4 148).
 template <bool S8, bool FAST, int N>
-__global__ void __launch_bounds__(kThreads, S8 ? 7 : 6)
+__global__ void __launch_bounds__(kThreads, S8 ? 5 : 6)
     k_adamw(const __grid_constant__ StepArgs<N> a) {
+  __shared__ Stage s_stage[S8 ? kWarps : 1][2];
   __shared__ StepConst s_k;
   __shared__ float s_lr;
   __shared__ int s_skip;
@@ -694,22 +744,62 @@ __global__ void __launch_bounds__(kThreads, S8 ? 7 : 6)
     k.decay = s_lr * q.weight_decay;
     const uint64_t key = split_mix(key0 + (uint64_t)t * kGolden);
     BlockAt at;
+    // 8-bit states: lane u has the scale byte of m of block b + u, lane 16 + u that of v
+    uint8_t* scale = lane < 16 ? q.m_scale : q.v_scale;
+    const int su = lane & 15;
+    int none = 0;
     if (!q.row_ids) {
       const int64_t whole = q.n / kBlockElems;
-      for (; b < whole; b += next) {
-        const int n = (int)min((int64_t)per, whole - b);
-        // lane u: the scale byte of m of block b + u, lane 16 + u: of v
-        uint8_t* scale = lane < 16 ? q.m_scale : q.v_scale;
-        int bytes = 0;
-        if (S8 && (lane & 15) < n) bytes = scale[b + (lane & 15)];
-        at.len = kBlockElems;
-        for (int u = 0; u < n; ++u) {
+      at.len = kBlockElems;
+      if (!S8) {
+        // (one block a group, but the loop over a group is what keeps this at 218 us: as a single
+        // loop it took 227)
+        for (; b < whole; b += next) {
+          const int n = (int)min((int64_t)per, whole - b);
+          for (int u = 0; u < n; ++u) {
+            at.block = b + u;
+            at.g0 = at.p0 = at.block * kBlockElems;
+            step_block<S8, FAST, true>(q, at, k, key, 0, none, nullptr);
+          }
+          if (b + n == whole) break;
+        }
+      } else if (b < whole) {
+        int n = (int)min((int64_t)per, whole - b), u = 0, stage = 0;
+        int bytes = su < n ? scale[b + su] : 0;
+        at.g0 = at.p0 = b * kBlockElems;
+        stage_block<FAST>(q, at, s_stage[warp][0]);
+        copy_commit();
+        for (bool more = true; more; stage ^= 1) {
+          // the block after this one: of this group, or the first of this warp's next group
+          int64_t b2 = b;
+          int n2 = n, u2 = u + 1, bytes2 = bytes;
+          if (u2 == n) {
+            b2 = b + next;
+            u2 = 0;
+            more = b2 < whole;
+            n2 = more ? (int)min((int64_t)per, whole - b2) : 0;
+            if (su < n2) bytes2 = scale[b2 + su];
+          }
+          __syncwarp();  // every lane has read the stage that is filled now
+          if (more) {
+            at.g0 = at.p0 = (b2 + u2) * kBlockElems;
+            stage_block<FAST>(q, at, s_stage[warp][stage ^ 1]);
+          }
+          copy_commit();
+          copy_wait_but_one();
+          __syncwarp();
           at.block = b + u;
           at.g0 = at.p0 = at.block * kBlockElems;
-          step_block<S8, FAST, true>(q, at, k, key, u, bytes);
+          step_block<S8, FAST, true>(q, at, k, key, u, bytes, &s_stage[warp][stage]);
+          if (u2 == 0) {
+            if (su < n) scale[b + su] = (uint8_t)bytes;
+            if (b + n == whole) break;
+            bytes = bytes2;
+          }
+          b = b2;
+          n = n2;
+          u = u2;
         }
-        if (S8 && (lane & 15) < n) scale[b + (lane & 15)] = (uint8_t)bytes;
-        if (b + n == whole) break;
       }
       // the shorter block behind the last whole one is with the warp whose turn it is
       at.len = (int)(q.n - whole * kBlockElems);
@@ -719,36 +809,54 @@ __global__ void __launch_bounds__(kThreads, S8 ? 7 : 6)
         step_block_any<S8>(q, at, k, key);
       }
     } else {
-      const int64_t rows = min(max(*q.n_rows, (int64_t)0), (int64_t)q.max_rows);
-      const int64_t di = next / q.row_blocks;
-      const int dj = (int)(next - di * q.row_blocks);
       RowWalk w;
+      w.rows = min(max(*q.n_rows, (int64_t)0), (int64_t)q.max_rows);
+      w.di = next / q.row_blocks;
+      w.dj = (int)(next - w.di * q.row_blocks);
       w.i = b / q.row_blocks;
       w.j = (int)(b - w.i * q.row_blocks);
-      ask_row(q, w, rows);
-      while (w.i < rows) {
-        const bool in = row_block(q, w, a.status, at);
-        w.i += di;
-        w.j += dj;
-        if (w.j >= q.row_blocks) {
-          w.j -= q.row_blocks;
-          ++w.i;
+      ask_row(q, w);
+      if (S8 && q.row_len % kBlockElems == 0) {  // whole blocks, 16-byte aligned whatever the types
+        bool have = next_block(q, w, a.status, at);
+        int bytes = 0, bytes2 = 0, stage = 0;
+        if (have) {
+          bytes = scale[at.block];
+          stage_block<FAST>(q, at, s_stage[warp][0]);
         }
-        ask_row(q, w, rows);
-        if (!in) continue;
-        if (q.row_len % 4) {
-          step_block_any<S8>(q, at, k, key);
-          continue;
+        copy_commit();
+        for (; have; stage ^= 1) {
+          BlockAt at2;
+          const bool more = next_block(q, w, a.status, at2);
+          __syncwarp();
+          if (more) {
+            bytes2 = scale[at2.block];
+            stage_block<FAST>(q, at2, s_stage[warp][stage ^ 1]);
+          }
+          copy_commit();
+          copy_wait_but_one();
+          __syncwarp();
+          step_block<S8, FAST, true>(q, at, k, key, 0, bytes, &s_stage[warp][stage]);
+          if (su == 0) scale[at.block] = (uint8_t)bytes;
+          at = at2;
+          bytes = bytes2;
+          have = more;
         }
-        uint8_t* scale = lane < 16 ? q.m_scale : q.v_scale;
-        int bytes = S8 ? scale[at.block] : 0;
-        if (at.len == kBlockElems)
-          step_block<S8, FAST, true>(q, at, k, key, 0, bytes);
-        else
-          step_block<S8, FAST, false>(q, at, k, key, 0, bytes);
-        if (S8 && (lane & 15) == 0) scale[at.block] = (uint8_t)bytes;
+      } else {
+        while (next_block(q, w, a.status, at)) {
+          if (q.row_len % 4) {
+            step_block_any<S8>(q, at, k, key);
+            continue;
+          }
+          int bytes = S8 ? scale[at.block] : 0;
+          if (!S8 && at.len == kBlockElems)
+            step_block<S8, FAST, !S8>(q, at, k, key, 0, bytes, nullptr);
+          else
+            step_block<S8, FAST, false>(q, at, k, key, 0, bytes, nullptr);
+          if (S8 && su == 0) scale[at.block] = (uint8_t)bytes;
+        }
       }
     }
+    if (S8) __syncwarp();  // every lane is done with the stages
   }
 }
 
@@ -763,7 +871,7 @@ hstu_status cuda_status(cudaError_t e, const char* where) {
   return HSTU_ERR_CUDA;
 }
 
-constexpr int kPerWarp = 8;
+constexpr int kPerWarp = 4;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
 // The gradient's part of a descriptor; *sparse: only some rows have one.
@@ -910,7 +1018,7 @@ hstu_status adamw(const hstu_adamw_args& h, const hstu_adamw_tensor* tensors, in
       if (!(kinds >> j & 1)) continue;
       LaunchScope ls(K_ADAMW, s);
       const int grid = (int)std::max<int64_t>(
-          1, std::min<int64_t>(a.chunks, num_sms() * (j >= 2 ? 7 : 16)));
+          1, std::min<int64_t>(a.chunks, num_sms() * (j >= 2 ? 5 : 16)));
       fn[j]<<<grid, kThreads, 0, s>>>(a);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");

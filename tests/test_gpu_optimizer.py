@@ -337,13 +337,14 @@ def test_touched_rows(R, d, U, cap, bits):
     assert torch.equal(t["m_scale"][others], old["m_scale"][others])
 
 
-def test_bad_rows_are_skipped_and_reported():
+@pytest.mark.parametrize("bits,d", [(32, 16), (8, 16), (8, 512), (32, 512), (8, 7)])
+def test_bad_rows_are_skipped_and_reported(bits, d):
     import torch
     import hstu_sequential_transducer_layer_b200 as H
     for ids, n, good in (([1, 5, 20], 3, [1, 5]), ([-1, 3, 4], 3, [3, 4]), ([2, 2, 6], 3, [2, 6]),
                          ([7, 3, 8], 3, [7, 8]), ([1, 2, 3], 4, [1, 2, 3]), ([1, 2, 3], -1, [])):
-        t = _make(0, "f32", "f32", False, 32, 1, shape=(10, 16))
-        t["grad"] = torch.ones(3, 16, device="cuda")
+        t = _make(0, "f32", "f32", False, bits, 1, shape=(10, d))
+        t["grad"] = torch.ones(3, d, device="cuda")
         t["row_ids"] = torch.tensor(ids, device="cuda")
         t["n_rows"] = torch.tensor([n], device="cuda")
         old, ws = _copy(t), _ws(256)
