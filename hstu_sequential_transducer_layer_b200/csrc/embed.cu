@@ -65,6 +65,13 @@ DEVI void load8(Raw8<HSTU_FP32>& r, const void* p, int64_t e) {
   r.a = __ldg(q);
   r.b = __ldg(q + 1);
 }
+// A lane's 8 elements from shared memory (fp32: their two halves 32 vectors apart).
+DEVI void from_shared(Raw8<HSTU_BF16>& r, const uint4* p) { r.a = *p; }
+DEVI void from_shared(Raw8<HSTU_FP16>& r, const uint4* p) { r.a = *p; }
+DEVI void from_shared(Raw8<HSTU_FP32>& r, const uint4* p) {
+  r.a = p[0];
+  r.b = p[32];
+}
 DEVI void widen(const Raw8<HSTU_BF16>& r, float (&f)[8]) {
   const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
@@ -767,6 +774,9 @@ struct Chain {
 template <int DT, bool VEC, bool PLAIN>
 __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const SumArgs a) {
   __shared__ float s_pre[kRunWarps][kColumns], s_post[kRunWarps][kColumns];
+  constexpr int kBatch = VEC && DT == HSTU_FP32 ? 2 : 4;  // rows
+  constexpr int kVecs = DT == HSTU_FP32 ? 2 : 1;          // 16 bytes of a row per lane
+  __shared__ uint4 s_rows[VEC ? kRunWarps : 1][2][kBatch][kVecs][32];
   __shared__ int s_flags[kRunWarps];  // 1: pre holds a part, 2: it goes on past this warp
   __shared__ Chain s_chain[2];        // of the run's first position, and of its last one
   grid_dep_launch();
@@ -795,20 +805,37 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
   int flags = 0;
-  // 8 rows of 16 bits in flight would spill at 64 registers (49 us of the touched rows of
-  // 38,070 x 1024 against 46); 6 warps a block, 6 blocks a SM: 56 registers and nothing spilled
-  // (dense gradient of 65,536 x 512: 69 us; 8 warps, 4 blocks: 72)
-  constexpr int kBatch = DT == HSTU_FP32 ? 2 : 4;
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
-    Raw8<DT> r[VEC ? kBatch : 1];
-    float one[VEC ? 1 : kBatch][8];
+  // Vector form: rows are copied into shared memory, each lane its own 16 bytes (32 of fp32), two
+  // groups of 2 KB ahead of the sums, where they take no registers: 6 warps a block, 6 blocks a
+  // SM, 56 registers (dense gradient of 65,536 x 512: 69.2 -> 67.6 us against 4 rows in registers;
+  // 7 blocks spill: 73.7).  A lane reads what it copied itself, so no exchange is needed.
+  const bool col = c0 + 8 * lane < a.d;
+  auto ask = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int64_t row = (int64_t)__shfl_sync(0xffffffffu, val, i0 + u + 1) * a.ld_dy + c0;
-      if (VEC) {
-        r[u] = Raw8<DT>{};
-        if (i0 + u < n && c0 + 8 * lane < a.d) load8(r[u], a.dY, row + 8 * lane);
-      } else {
+      const uint32_t t = __shfl_sync(0xffffffffu, val, (i0 + u + 1) & 31);
+      if (i0 + u < n && col) {
+        const uint8_t* src = static_cast<const uint8_t*>(a.dY) +
+                             ((int64_t)t * a.ld_dy + c0 + 8 * lane) * (DT == HSTU_FP32 ? 4 : 2);
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q)
+          copy16(&s_rows[warp][(i0 / kBatch) & 1][u][q][lane], src + 16 * q);
+      }
+    }
+    copy_commit();
+  };
+  if (VEC) {
+    ask(0);
+    ask(kBatch);
+  }
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    float one[VEC ? 1 : kBatch][8];
+    if (VEC) {
+      copy_wait_but_one();
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t row = (int64_t)__shfl_sync(0xffffffffu, val, i0 + u + 1) * a.ld_dy + c0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int c = 32 * j + lane;
@@ -820,7 +847,8 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + u;
-      if (i < n && i > 0 && (heads >> i & 1)) {  // the running segment ended with token i - 1
+      if (i >= n) break;
+      if (i > 0 && (heads >> i & 1)) {  // the running segment ended with token i - 1
         if (open) {
           put8(s_pre[warp], lane, acc);
           flags = 1;
@@ -832,11 +860,19 @@ __global__ void __launch_bounds__(kRunWarps * 32, VEC ? 6 : 3) k_embed_sum(const
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.f;
       }
-      float x[8];
-      if (VEC) widen(r[u], x);
+      if (VEC) {
+        Raw8<DT> r;
+        float x[8];
+        from_shared(r, &s_rows[warp][(i0 / kBatch) & 1][u][0][lane]);
+        widen(r, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += VEC ? x[j] : one[u][j];
+        for (int j = 0; j < 8; ++j) acc[j] += x[j];  // columns past the end: not written
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += one[u][j];
+      }
     }
+    if (VEC) ask(i0 + 2 * kBatch);
   }
   bool post = false;
   if (n > 0) {

@@ -417,13 +417,6 @@ DEVI void store_param(const StepTensor& q, int64_t at, const float (&p)[4]) {
 struct Stage {
   uint4 g[64], p[64], m[16], v[16];  // 16-bit gradients and parameters: half
 };
-DEVI void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
-               : "memory");
-}
-DEVI void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All copies but those of the last commit have arrived.
-DEVI void copy_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 template <bool FAST>
 DEVI void stage_block(const StepTensor& q, const BlockAt& at, Stage& s) {
@@ -441,11 +434,11 @@ DEVI void stage_block(const StepTensor& q, const BlockAt& at, Stage& s) {
 }
 
 // The step of one block whose length is a multiple of 4 and whose rows are
-// 16-byte aligned.  WHOLE: 256 elements; with 8-bit states staged.  Lane l holds elements 4 l + 128 j +
-// (0..3), j = 0, 1, so every access of a warp is to consecutive addresses;
-// all of a lane's loads are issued before the first one is used.  8-bit
-// states: the block's scale bytes are `bytes` of lanes u (m) and 16 + u (v), and
-// are replaced by the new ones.
+// 16-byte aligned.  WHOLE: 256 elements; with 8-bit states staged.  Lane l
+// holds elements 4 l + 128 j + (0..3), j = 0, 1, so every access of a warp is to
+// consecutive addresses; all of a lane's loads are issued before the first one
+// is used.  8-bit states: the block's scale bytes are `bytes` of lanes u (m) and
+// 16 + u (v), and are replaced by the new ones.
 template <bool S8, bool FAST, bool WHOLE>
 DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k, uint64_t key,
                      int u, int& bytes, const Stage* st) {
@@ -767,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, S8 ? 5 : 6)
         int n = (int)min((int64_t)per, whole - b), u = 0, stage = 0;
         int bytes = su < n ? scale[b + su] : 0;
         at.g0 = at.p0 = b * kBlockElems;
+        __syncwarp();  // every lane is through with the tensor before
         stage_block<FAST>(q, at, s_stage[warp][0]);
         copy_commit();
         for (bool more = true; more; stage ^= 1) {
@@ -819,6 +813,7 @@ __global__ void __launch_bounds__(kThreads, S8 ? 5 : 6)
       if (S8 && q.row_len % kBlockElems == 0) {  // whole blocks, 16-byte aligned whatever the types
         bool have = next_block(q, w, a.status, at);
         int bytes = 0, bytes2 = 0, stage = 0;
+        __syncwarp();
         if (have) {
           bytes = scale[at.block];
           stage_block<FAST>(q, at, s_stage[warp][0]);

@@ -24,6 +24,15 @@ DEVI uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// Copies of 16 bytes from global into shared memory, counted per thread.
+DEVI void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+               : "memory");
+}
+DEVI void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All of this thread's copies but those of its last commit have arrived.
+DEVI void copy_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
 // Shared-space loads and stores by 32-bit shared-window address: no generic
 // address resolution, and loads are tracked with the short (shared-memory)
 // latency.  The "memory" clobber keeps them ordered with the surrounding
