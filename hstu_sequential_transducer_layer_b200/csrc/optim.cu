@@ -266,17 +266,15 @@ DEVI uint64_t split_mix(uint64_t z) {
   return z ^ (z >> 31);
 }
 
-// e4m3 code of the magnitude t (scaled, below 2^8), rounded up when the
-// 16-bit number r / 2^16 reaches the missing part: an e4m3 code step is 2^20
-// units of fp32's significand, so r * 16 is added and the rest cut.  Below
-// 2^-6 the codes have a fixed step, which adding 2^-6 gives them.  Everything
-// is 4 bits further up, so that the code is the top byte and what is cut the
-// 24 bits below it; r8 is r shifted left by 8.
-DEVI uint32_t e4m3_up(float t, uint32_t r8) {
-  const bool sub = t < 0.015625f;
-  t = sub ? __fadd_rn(t, 0.015625f) : t;
-  return (__float_as_uint(t) << 4) + r8 - (sub ? 0xC8000000u : 0xC0000000u);
-}
+// e4m3 code of the magnitude of x = 2^-120 t, |t| < 2^8, rounded up when the
+// 16-bit number r / 2^16 reaches the missing part.  The factor turns fp32's
+// exponent field into e4m3's (bias 127 - 120 = 7) and its subnormal numbers
+// into e4m3's (both have the fixed step of the smallest exponent), so the code
+// is what lies above the lowest 20 bits, and r * 16 is added before they are
+// cut.  Everything is 4 bits further up, so that the sign falls off and the
+// code is the top byte; r8 is r shifted left by 8.
+constexpr float kCodeScale = 7.5231638452626400e-37f;  // 2^-120
+DEVI uint32_t e4m3_up(float x, uint32_t r8) { return (__float_as_uint(x) << 4) + r8; }
 // Top bytes of four words.
 DEVI uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
@@ -345,21 +343,51 @@ DEVI void store_elem(int dtype, void* p, int64_t i, float x) {
     static_cast<__half*>(p)[i] = __float2half_rn(x);
 }
 
+// Two fp32 operations in one instruction, each rounded as the single one.  The
+// 8-bit step is bound by the instructions it issues: with these and a shorter
+// encoding 42M parameters take 141 instead of 147 us, and 152 instead of 161
+// under the power limit.
+DEVI float2 both(float x) { return make_float2(x, x); }
+DEVI float2 mul2(float2 x, float2 y) {
+  float2 z;
+  asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
+      "mul.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
+      : "=f"(z.x), "=f"(z.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return z;
+}
+DEVI float2 fma2(float2 x, float2 y, float2 w) {
+  float2 z;
+  asm("{\n.reg .b64 x, y, w, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
+      "mov.b64 w, {%6, %7};\nfma.rn.f32x2 z, x, y, w;\nmov.b64 {%0, %1}, z;\n}"
+      : "=f"(z.x), "=f"(z.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(w.x), "f"(w.y));
+  return z;
+}
+
 // What all elements of a step share.
 struct StepConst {
   float b1, omb1, b2, omb2, eps, gs, step_size, rbc2, decay;
 };
 
 // m and v after the step.  Products and sums are kept apart (no contraction),
-// so that an 8-bit state does not depend on how the compiler fuses them.
-DEVI void moments(const StepConst& k, float g, float& m, float& v) {
-  g = __fmul_rn(g, k.gs);
-  m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.omb1));
-  v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.omb2));
+// so that an 8-bit state does not depend on how the compiler fuses them; the
+// sums are single instructions because add.rn.f32x2 behind mul.rn.f32x2 does
+// get fused (seen in the results).
+DEVI float2 add_apart(float2 x, float2 y) {
+  return make_float2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
 }
-// The new parameter; eps >= 2^-126, so the denominator is a normal number.
-DEVI float new_param(const StepConst& k, float p, float m, float root) {
-  return p - fmaf(p, k.decay, m * rcp_approx(fmaf(root, k.rbc2, k.eps)) * k.step_size);
+DEVI void moments(const StepConst& k, float2 g, float2& m, float2& v) {
+  g = mul2(g, both(k.gs));
+  m = add_apart(mul2(m, both(k.b1)), mul2(g, both(k.omb1)));
+  v = add_apart(mul2(v, both(k.b2)), mul2(mul2(g, g), both(k.omb2)));
+}
+// The new parameters; eps >= 2^-126, so the denominator is a normal number.
+DEVI float2 new_param(const StepConst& k, float2 p, float2 m, float2 root) {
+  const float2 d = fma2(root, both(k.rbc2), both(k.eps));
+  const float2 step =
+      mul2(mul2(m, make_float2(rcp_approx(d.x), rcp_approx(d.y))), both(k.step_size));
+  return fma2(fma2(p, both(k.decay), step), both(-1.f), p);
 }
 
 // Key of a block's random numbers, and an element's 32 random bits: the low
@@ -413,7 +441,7 @@ DEVI void store_param(const StepTensor& q, int64_t at, const float (&p)[4]) {
 // shared memory one block ahead of the arithmetic (two stages per warp).  The
 // arithmetic is long enough that a warp's loads have to be in flight
 // meanwhile, and has no registers to hold them: 160 -> 146 us for 42M
-// parameters.  (fp32 states: 224 us against 218 without it.)
+// parameters when it was added.  (fp32 states: 224 us against 218 without it.)
 struct Stage {
   uint4 g[64], p[64], m[16], v[16];  // 16-bit gradients and parameters: half
 };
@@ -486,29 +514,30 @@ DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k,
     float g[4], p[4];
     widen4(FAST ? HSTU_FP32 : q.grad_dtype, gr[j], g);
     widen4(pw ? HSTU_FP32 : q.param_dtype, pr[j], p);
-    if (S8) {
-      const float2 m0 = e4m3x2_to_f32(mr[j].x & 0xffffu), m1 = e4m3x2_to_f32(mr[j].x >> 16);
-      const float2 v0 = e4m3x2_to_f32(vr[j].x & 0xffffu), v1 = e4m3x2_to_f32(vr[j].x >> 16);
-      m[j][0] = m0.x, m[j][1] = m0.y, m[j][2] = m1.x, m[j][3] = m1.y;
-      v[j][0] = v0.x, v[j][1] = v0.y, v[j][2] = v1.x, v[j][3] = v1.y;
-    } else {
+    if (!S8) {
       widen4(HSTU_FP32, mr[j], m[j]);
       widen4(HSTU_FP32, vr[j], v[j]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; i += 2) {
+      float2 m2, v2;
       if (S8) {
-        m[j][i] = __fmul_rn(m[j][i], ms);
-        v[j][i] = __fmul_rn(v[j][i], vs);
-        v[j][i] = __fmul_rn(v[j][i], v[j][i]);
+        m2 = mul2(e4m3x2_to_f32(mr[j].x >> (8 * i) & 0xffffu), both(ms));
+        v2 = mul2(e4m3x2_to_f32(vr[j].x >> (8 * i) & 0xffffu), both(vs));
+        v2 = mul2(v2, v2);
+      } else {
+        m2 = make_float2(m[j][i], m[j][i + 1]);
+        v2 = make_float2(v[j][i], v[j][i + 1]);
       }
-      moments(k, g[i], m[j][i], v[j][i]);
-      const float root = __fsqrt_rn(v[j][i]);
-      p[i] = new_param(k, p[i], m[j][i], root);
+      moments(k, make_float2(g[i], g[i + 1]), m2, v2);
+      const float2 root = make_float2(__fsqrt_rn(v2.x), __fsqrt_rn(v2.y));
+      const float2 p2 = new_param(k, make_float2(p[i], p[i + 1]), m2, root);
+      p[i] = p2.x, p[i + 1] = p2.y;
+      m[j][i] = m2.x, m[j][i + 1] = m2.y;
+      v[j][i] = S8 ? root.x : v2.x, v[j][i + 1] = S8 ? root.y : v2.y;
       if (S8) {
-        v[j][i] = root;
-        top_m = max_abs(top_m, m[j][i]);
-        top_r = max_abs(top_r, root);
+        top_m = max_abs(max_abs(top_m, m2.x), m2.y);
+        top_r = max_abs(max_abs(top_r, root.x), root.y);
       }
     }
     if (!WHOLE && e >= at.len) continue;
@@ -553,10 +582,13 @@ DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k,
     if (!WHOLE && e >= at.len) continue;
     uint32_t a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = elem_random(base, 128 * j + i);
-      a[i] = e4m3_up(fabsf(m[j][i]) * mi, low16_up(r));
-      b[i] = e4m3_up(v[j][i] * vi, high16_up(r));
+    for (int i = 0; i < 4; i += 2) {
+      // (two factors: their product can be below fp32's range)
+      const float2 x = mul2(mul2(make_float2(m[j][i], m[j][i + 1]), both(mi)), both(kCodeScale));
+      const float2 y = mul2(mul2(make_float2(v[j][i], v[j][i + 1]), both(vi)), both(kCodeScale));
+      const uint32_t r0 = elem_random(base, 128 * j + i), r1 = elem_random(base, 128 * j + i + 1);
+      a[i] = e4m3_up(x.x, low16_up(r0)), a[i + 1] = e4m3_up(x.y, low16_up(r1));
+      b[i] = e4m3_up(y.x, high16_up(r0)), b[i + 1] = e4m3_up(y.y, high16_up(r1));
     }
     const uint32_t sign = top_bytes(__float_as_uint(m[j][0]), __float_as_uint(m[j][1]),
                                     __float_as_uint(m[j][2]), __float_as_uint(m[j][3]));
@@ -595,9 +627,11 @@ DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst
       m[i] = static_cast<float*>(q.m)[x];
       v = static_cast<float*>(q.v)[x];
     }
-    moments(k, g, m[i], v);
+    float2 m2 = both(m[i]), v2 = both(v);
+    moments(k, both(g), m2, v2);
+    m[i] = m2.x, v = v2.x;
     root[i] = __fsqrt_rn(v);
-    p = new_param(k, p, m[i], root[i]);
+    p = new_param(k, both(p), m2, both(root[i])).x;
     if (!S8) {
       static_cast<float*>(q.m)[x] = m[i];
       static_cast<float*>(q.v)[x] = v;
@@ -622,9 +656,9 @@ DEVI void step_block_any(const StepTensor& q, const BlockAt& at, const StepConst
     const int e = lane + 32 * i;
     if (e >= at.len) continue;
     const uint32_t r = elem_random(base, e);
-    const uint32_t a = abs_bits(m[i]) < kInfBits ? e4m3_up(fabsf(m[i]) * mi, low16_up(r)) >> 24
+    const uint32_t a = abs_bits(m[i]) < kInfBits ? e4m3_up(m[i] * mi * kCodeScale, low16_up(r)) >> 24
                                                  : 0x7fu;
-    const uint32_t b = abs_bits(root[i]) < kInfBits ? e4m3_up(root[i] * vi, high16_up(r)) >> 24
+    const uint32_t b = abs_bits(root[i]) < kInfBits ? e4m3_up(root[i] * vi * kCodeScale, high16_up(r)) >> 24
                                                     : 0x7fu;
     static_cast<uint8_t*>(q.m)[at.p0 + e] =
         (uint8_t)(a | ((__float_as_uint(m[i]) >> 24) & 0x80u));
@@ -682,11 +716,16 @@ DEVI bool next_block(const StepTensor& q, RowWalk& w, int* status, BlockAt& at) 
 // Thread blocks of 128 threads per SM, measured on 42M parameters: fp32 states
 // 6 resident (80 registers) and 16 launched (218 us, 6.2 TB/s; 8 resident at 64
 // registers 235; no more launched than resident 228: the hardware's handing
-// out of thread blocks evens out what a fixed share does not); 8-bit states,
-// bound by instructions (about 95 per element) as much as by memory, 5
-// resident and launched (146 us, 5.8 TB/s; 7, which spill, 166; 4 148).
+// out of thread blocks evens out what a fixed share does not).  8-bit states,
+// bound by instructions as much as by memory: with fp32 gradients and
+// parameters 4 resident and launched (141 us, 6.0 TB/s; 152 once the power limit
+// holds the clock at 1.75 GHz; 5: 150 and 151; 8 launched 149), else, where a
+// tensor is more likely a table whose rows take two dependent loads, 5 (14,011
+// rows of 512: 31 us; 4: 33).
+constexpr int resident(bool s8, bool fast) { return !s8 ? 6 : fast ? 4 : 5; }
+
 template <bool S8, bool FAST, int N>
-__global__ void __launch_bounds__(kThreads, S8 ? 5 : 6)
+__global__ void __launch_bounds__(kThreads, resident(S8, FAST))
     k_adamw(const __grid_constant__ StepArgs<N> a) {
   __shared__ Stage s_stage[S8 ? kWarps : 1][2];
   __shared__ StepConst s_k;
@@ -1013,7 +1052,7 @@ hstu_status adamw(const hstu_adamw_args& h, const hstu_adamw_tensor* tensors, in
       if (!(kinds >> j & 1)) continue;
       LaunchScope ls(K_ADAMW, s);
       const int grid = (int)std::max<int64_t>(
-          1, std::min<int64_t>(a.chunks, num_sms() * (j >= 2 ? 5 : 16)));
+          1, std::min<int64_t>(a.chunks, num_sms() * (j >= 2 ? resident(true, j & 1) : 16)));
       fn[j]<<<grid, kThreads, 0, s>>>(a);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");

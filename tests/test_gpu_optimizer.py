@@ -138,6 +138,28 @@ def _copy(t):
     return {k: (x.clone() if hasattr(x, "clone") else x) for k, x in t.items()}
 
 
+@pytest.mark.parametrize("shape", [(256 * 9,), (256 * 9 + 101,), (40, 257), (40, 512)])
+def test_states_are_not_contracted(shape):
+    """fp32 m and v equal products and sums that are rounded one by one, bit for bit."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    t = _make(0, "f32", "f32", False, 32, 3, shape=shape)
+    if len(shape) == 2:
+        t["row_ids"] = torch.arange(shape[0], device="cuda")
+        t["n_rows"] = torch.tensor([shape[0]], device="cuda")
+    g, m, v = (t[k].cpu().numpy() for k in ("grad", "m", "v"))
+    ws = _ws(256)
+    H.hstu_adamw_step(H.AdamWTensors([t]), ws, step=2, **HYPER)
+    assert H.hstu_read_status(ws) == 0
+    f = np.float32
+    b1, b2 = HYPER["beta1"], HYPER["beta2"]
+    rm = m * f(b1) + g * f(1 - b1)
+    rv = v * f(b2) + g * g * f(1 - b2)
+    assert rm.dtype == f and rv.dtype == f
+    np.testing.assert_array_equal(t["m"].cpu().numpy(), rm)
+    np.testing.assert_array_equal(t["v"].cpu().numpy(), rv)
+
+
 def _blocks(x, rows=None):
     """Array [blocks, 256] of a tensor (of each row of it), zeros behind the end."""
     x = x.reshape(1, -1) if rows is None else x.reshape(rows, -1)
