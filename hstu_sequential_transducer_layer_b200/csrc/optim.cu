@@ -229,7 +229,7 @@ struct StepTensor {
   float weight_decay;
   uint8_t grad_dtype, param_dtype;
   uint8_t per;             // consecutive blocks that a warp takes (<= 16)
-  uint8_t kind;            // 2 * (8-bit states) + (gradient and parameter read are fp32)
+  uint8_t kind;            // kTypes * (8-bit states) + its Types
 };
 
 template <int N>
@@ -406,30 +406,35 @@ struct BlockAt {
   int len;
 };
 
-// Where a tensor's elements are read: FAST tensors (the gradient and the
-// parameter that is read -- the master, or the parameter itself -- are fp32,
-// as this library's backward pass and trainer have them) need no type asked
-// for in the loop.
-template <bool FAST>
-DEVI bool grad_wide(const StepTensor& q) { return FAST || q.grad_dtype == HSTU_FP32; }
-template <bool FAST>
+// Types of a tensor that the loop need not ask for: kWide, the gradient and the
+// parameter that is read (the master, or the parameter itself) are fp32, as
+// this library's backward pass and trainer have them; kTable, fp32 gradients of
+// a bf16 parameter without a master (an embedding table).  With the questions
+// in the loop its code no longer fits the instruction cache next to the SM's
+// partitions: touched rows of 8-bit states 27 us instead of 31.
+enum Types { kAny = 0, kWide = 1, kTable = 2, kTypes = 3 };
+template <int TY>
+DEVI bool grad_wide(const StepTensor& q) { return TY != kAny || q.grad_dtype == HSTU_FP32; }
+template <int TY>
 DEVI bool param_wide(const StepTensor& q) {
-  return FAST || q.master || q.param_dtype == HSTU_FP32;
+  return TY == kWide || (TY == kAny && (q.master || q.param_dtype == HSTU_FP32));
 }
+template <int TY>
+DEVI int param_type(const StepTensor& q) { return TY == kTable ? HSTU_BF16 : q.param_dtype; }
 
 // Stores four new parameters and what is kept of them.
-template <bool FAST>
+template <int TY>
 DEVI void store_param(const StepTensor& q, int64_t at, const float (&p)[4]) {
-  if (param_wide<FAST>(q))
+  if (param_wide<TY>(q))
     *reinterpret_cast<float4*>(static_cast<float*>(q.master ? q.master : q.param) + at) =
         make_float4(p[0], p[1], p[2], p[3]);
   float2 x = make_float2(p[0], p[1]), y = make_float2(p[2], p[3]);  // as stored
-  if (q.param_dtype == HSTU_BF16) {
+  if (param_type<TY>(q) == HSTU_BF16) {
     const __nv_bfloat162 s = __floats2bfloat162_rn(x.x, x.y), t = __floats2bfloat162_rn(y.x, y.y);
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(q.param) + at) =
         make_uint2(bits2(s), bits2(t));
     x = __bfloat1622float2(s), y = __bfloat1622float2(t);
-  } else if (q.param_dtype == HSTU_FP16) {
+  } else if (param_type<TY>(q) == HSTU_FP16) {
     const __half2 s = __floats2half2_rn(x.x, x.y), t = __floats2half2_rn(y.x, y.y);
     *reinterpret_cast<uint2*>(static_cast<__half*>(q.param) + at) = make_uint2(bits2(s), bits2(t));
     x = __half22float2(s), y = __half22float2(t);
@@ -446,10 +451,10 @@ struct Stage {
   uint4 g[64], p[64], m[16], v[16];  // 16-bit gradients and parameters: half
 };
 
-template <bool FAST>
+template <int TY>
 DEVI void stage_block(const StepTensor& q, const BlockAt& at, Stage& s) {
   const int lane = threadIdx.x & 31;
-  const bool gw = grad_wide<FAST>(q), pw = param_wide<FAST>(q);
+  const bool gw = grad_wide<TY>(q), pw = param_wide<TY>(q);
   const uint8_t* gp = static_cast<const uint8_t*>(q.grad) + (at.g0 << (gw ? 2 : 1)) + 16 * lane;
   const uint8_t* wp = static_cast<const uint8_t*>(q.master ? q.master : q.param) +
                       (at.p0 << (pw ? 2 : 1)) + 16 * lane;
@@ -467,11 +472,11 @@ DEVI void stage_block(const StepTensor& q, const BlockAt& at, Stage& s) {
 // consecutive addresses; all of a lane's loads are issued before the first one
 // is used.  8-bit states: the block's scale bytes are `bytes` of lanes u (m) and
 // 16 + u (v), and are replaced by the new ones.
-template <bool S8, bool FAST, bool WHOLE>
+template <bool S8, int TY, bool WHOLE>
 DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k, uint64_t key,
                      int u, int& bytes, const Stage* st) {
   const int lane = threadIdx.x & 31;
-  const bool gw = grad_wide<FAST>(q), pw = param_wide<FAST>(q);
+  const bool gw = grad_wide<TY>(q), pw = param_wide<TY>(q);
   const uint8_t* gp = static_cast<const uint8_t*>(q.grad) + (at.g0 << (gw ? 2 : 1));
   const uint8_t* wp = static_cast<const uint8_t*>(q.master ? q.master : q.param) +
                       (at.p0 << (pw ? 2 : 1));
@@ -512,8 +517,8 @@ DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k,
   for (int j = 0; j < 2; ++j) {
     const int e = 4 * lane + 128 * j;
     float g[4], p[4];
-    widen4(FAST ? HSTU_FP32 : q.grad_dtype, gr[j], g);
-    widen4(pw ? HSTU_FP32 : q.param_dtype, pr[j], p);
+    widen4(TY != kAny ? HSTU_FP32 : q.grad_dtype, gr[j], g);
+    widen4(pw ? HSTU_FP32 : param_type<TY>(q), pr[j], p);
     if (!S8) {
       widen4(HSTU_FP32, mr[j], m[j]);
       widen4(HSTU_FP32, vr[j], v[j]);
@@ -545,7 +550,7 @@ DEVI void step_block(const StepTensor& q, const BlockAt& at, const StepConst& k,
       *reinterpret_cast<float4*>(mp + 4 * e) = make_float4(m[j][0], m[j][1], m[j][2], m[j][3]);
       *reinterpret_cast<float4*>(vp + 4 * e) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
     }
-    store_param<FAST>(q, at.p0 + e, p);
+    store_param<TY>(q, at.p0 + e, p);
   }
   if (!S8) return;
   uint32_t tm = __reduce_max_sync(0xffffffffu, abs_bits(top_m));
@@ -704,7 +709,7 @@ DEVI bool next_block(const StepTensor& q, RowWalk& w, int* status, BlockAt& at) 
 }
 
 // One step of every tensor of the list whose states have this width and whose
-// types are FAST or not, a warp per block of 256 elements.  Bandwidth-bound:
+// types are of this sort, a warp per block of 256 elements.  Bandwidth-bound:
 // per element the gradient, the states and the (master) parameter are read
 // once and the results written once.
 //
@@ -721,11 +726,11 @@ DEVI bool next_block(const StepTensor& q, RowWalk& w, int* status, BlockAt& at) 
 // parameters 4 resident and launched (141 us, 6.0 TB/s; 152 once the power limit
 // holds the clock at 1.75 GHz; 5: 150 and 151; 8 launched 149), else, where a
 // tensor is more likely a table whose rows take two dependent loads, 5 (14,011
-// rows of 512: 31 us; 4: 33).
-constexpr int resident(bool s8, bool fast) { return !s8 ? 6 : fast ? 4 : 5; }
+// rows of 512: 27 us; 4 or 6: 29).
+constexpr int resident(bool s8, int types) { return !s8 ? 6 : types == kWide ? 4 : 5; }
 
-template <bool S8, bool FAST, int N>
-__global__ void __launch_bounds__(kThreads, resident(S8, FAST))
+template <bool S8, int TY, int N>
+__global__ void __launch_bounds__(kThreads, resident(S8, TY))
     k_adamw(const __grid_constant__ StepArgs<N> a) {
   __shared__ Stage s_stage[S8 ? kWarps : 1][2];
   __shared__ StepConst s_k;
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, resident(S8, FAST))
     int64_t b = ((c - q.chunk0) * kWarps + warp) * per;
     const int64_t next = (int64_t)gridDim.x * kWarps * per;
     c += (end - c + gridDim.x - 1) / gridDim.x * gridDim.x;
-    if (q.kind != 2 * S8 + FAST) continue;
+    if (q.kind != kTypes * S8 + TY) continue;
     k.decay = s_lr * q.weight_decay;
     const uint64_t key = split_mix(key0 + (uint64_t)t * kGolden);
     BlockAt at;
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, resident(S8, FAST))
           for (int u = 0; u < n; ++u) {
             at.block = b + u;
             at.g0 = at.p0 = at.block * kBlockElems;
-            step_block<S8, FAST, true>(q, at, k, key, 0, none, nullptr);
+            step_block<S8, TY, true>(q, at, k, key, 0, none, nullptr);
           }
           if (b + n == whole) break;
         }
@@ -800,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, resident(S8, FAST))
         int bytes = su < n ? scale[b + su] : 0;
         at.g0 = at.p0 = b * kBlockElems;
         __syncwarp();  // every lane is through with the tensor before
-        stage_block<FAST>(q, at, s_stage[warp][0]);
+        stage_block<TY>(q, at, s_stage[warp][0]);
         copy_commit();
         for (bool more = true; more; stage ^= 1) {
           // the block after this one: of this group, or the first of this warp's next group
@@ -816,14 +821,14 @@ __global__ void __launch_bounds__(kThreads, resident(S8, FAST))
           __syncwarp();  // every lane has read the stage that is filled now
           if (more) {
             at.g0 = at.p0 = (b2 + u2) * kBlockElems;
-            stage_block<FAST>(q, at, s_stage[warp][stage ^ 1]);
+            stage_block<TY>(q, at, s_stage[warp][stage ^ 1]);
           }
           copy_commit();
           copy_wait_but_one();
           __syncwarp();
           at.block = b + u;
           at.g0 = at.p0 = at.block * kBlockElems;
-          step_block<S8, FAST, true>(q, at, k, key, u, bytes, &s_stage[warp][stage]);
+          step_block<S8, TY, true>(q, at, k, key, u, bytes, &s_stage[warp][stage]);
           if (u2 == 0) {
             if (su < n) scale[b + su] = (uint8_t)bytes;
             if (b + n == whole) break;
@@ -855,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, resident(S8, FAST))
         __syncwarp();
         if (have) {
           bytes = scale[at.block];
-          stage_block<FAST>(q, at, s_stage[warp][0]);
+          stage_block<TY>(q, at, s_stage[warp][0]);
         }
         copy_commit();
         for (; have; stage ^= 1) {
@@ -864,12 +869,12 @@ __global__ void __launch_bounds__(kThreads, resident(S8, FAST))
           __syncwarp();
           if (more) {
             bytes2 = scale[at2.block];
-            stage_block<FAST>(q, at2, s_stage[warp][stage ^ 1]);
+            stage_block<TY>(q, at2, s_stage[warp][stage ^ 1]);
           }
           copy_commit();
           copy_wait_but_one();
           __syncwarp();
-          step_block<S8, FAST, true>(q, at, k, key, 0, bytes, &s_stage[warp][stage]);
+          step_block<S8, TY, true>(q, at, k, key, 0, bytes, &s_stage[warp][stage]);
           if (su == 0) scale[at.block] = (uint8_t)bytes;
           at = at2;
           bytes = bytes2;
@@ -883,9 +888,9 @@ __global__ void __launch_bounds__(kThreads, resident(S8, FAST))
           }
           int bytes = S8 ? scale[at.block] : 0;
           if (!S8 && at.len == kBlockElems)
-            step_block<S8, FAST, !S8>(q, at, k, key, 0, bytes, nullptr);
+            step_block<S8, TY, !S8>(q, at, k, key, 0, bytes, nullptr);
           else
-            step_block<S8, FAST, false>(q, at, k, key, 0, bytes, nullptr);
+            step_block<S8, TY, false>(q, at, k, key, 0, bytes, nullptr);
           if (S8 && su == 0) scale[at.block] = (uint8_t)bytes;
         }
       }
@@ -1036,8 +1041,11 @@ hstu_status adamw(const hstu_adamw_args& h, const hstu_adamw_tensor* tensors, in
       q.weight_decay = (float)t.weight_decay;
       q.grad_dtype = (uint8_t)t.grad_dtype;
       q.param_dtype = (uint8_t)t.param_dtype;
-      q.kind = (uint8_t)(2 * (t.state_bits == 8) +
-                         (t.grad_dtype == HSTU_FP32 && (q.master || t.param_dtype == HSTU_FP32)));
+      const int types = t.grad_dtype != HSTU_FP32                   ? kAny
+                        : q.master || t.param_dtype == HSTU_FP32 ? kWide
+                        : t.param_dtype == HSTU_BF16             ? kTable
+                                                                 : kAny;
+      q.kind = (uint8_t)(kTypes * (t.state_bits == 8) + types);
       q.per = large && t.state_bits == 8 && !t.row_ids ? kPerWarp : 1;
       const int64_t chunk = kWarps * q.per;
       a.chunks += (tensor_blocks(t) + chunk - 1) / chunk;
@@ -1045,14 +1053,14 @@ hstu_status adamw(const hstu_adamw_args& h, const hstu_adamw_tensor* tensors, in
     // a kernel per kind of tensor: one list seldom has more than one or two
     unsigned kinds = a.n == 0 ? 1u : 0u;
     for (int j = 0; j < a.n; ++j) kinds |= 1u << a.t[j].kind;
-    static void (*const fn[4])(StepArgs<N>) = {
-        k_adamw<false, false, N>, k_adamw<false, true, N>, k_adamw<true, false, N>,
-        k_adamw<true, true, N>};
-    for (int j = 0; j < 4; ++j) {
+    static void (*const fn[2 * kTypes])(StepArgs<N>) = {
+        k_adamw<false, kAny, N>, k_adamw<false, kWide, N>, k_adamw<false, kTable, N>,
+        k_adamw<true, kAny, N>,  k_adamw<true, kWide, N>,  k_adamw<true, kTable, N>};
+    for (int j = 0; j < 2 * kTypes; ++j) {
       if (!(kinds >> j & 1)) continue;
       LaunchScope ls(K_ADAMW, s);
       const int grid = (int)std::max<int64_t>(
-          1, std::min<int64_t>(a.chunks, num_sms() * (j >= 2 ? resident(true, j & 1) : 16)));
+          1, std::min<int64_t>(a.chunks, num_sms() * (j >= kTypes ? resident(true, j % kTypes) : 16)));
       fn[j]<<<grid, kThreads, 0, s>>>(a);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");
