@@ -562,6 +562,7 @@ class GradTensors:
         if t.get("n_rows") is not None:
             _need(g.dim() == 2, w, "grad with n_rows: a matrix")
             _i64(t["n_rows"], w, "n_rows")
+            _need(t["n_rows"].numel() == 1, w, "n_rows: int64 [1]")
             c.n_rows = self._take(t["n_rows"], "n_rows")
             c.max_rows, c.row_len = g.shape
 

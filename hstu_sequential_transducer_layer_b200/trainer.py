@@ -83,13 +83,13 @@ class HSTUTrainer:
         rate (default: the constructor's).  Returns dX; `norm` holds the
         gradient norm and the clip factor.  A step whose gradients are not all
         finite (clip factor NaN) changes nothing, but is counted in `steps`."""
-        dX, _ = self.runner.stack_bwd(offsets, X, timestamps, dY, max_len, grads=self.grads,
-                                      stream=stream)
         if (ids is None) != (self.table is None):
             raise _b.HstuError(1, "HSTUTrainer.step: ids and a table come together")
+        if ids is not None and ids.numel() > self.max_tokens:
+            raise _b.HstuError(3, "HSTUTrainer.step: more tokens than max_tokens")
+        dX, _ = self.runner.stack_bwd(offsets, X, timestamps, dY, max_len, grads=self.grads,
+                                      stream=stream)
         if ids is not None:
-            if ids.numel() > self.max_tokens:
-                raise _b.HstuError(3, "HSTUTrainer.step: more tokens than max_tokens")
             _b.hstu_embed_bwd_rows(ids, dX, self.table.shape[0], self.row_ids, self.row_grad,
                                    self.n_rows, self._ews, scale=embed_scale, pad_id=pad_id,
                                    stream=stream)

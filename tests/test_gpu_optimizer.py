@@ -205,7 +205,8 @@ SIZES = [1, 3, 255, 256, 257, 2047, 2048, 2051, 70001]
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("param,grad,master", [("bf16", "f32", True), ("bf16", "bf16", False),
                                                ("f32", "f32", False), ("f16", "f16", True),
-                                               ("f32", "bf16", False), ("f16", "f32", False)])
+                                               ("f32", "bf16", False), ("f16", "f32", False),
+                                               ("bf16", "f32", False)])
 def test_adamw_step(bits, param, grad, master):
     import torch
     import hstu_sequential_transducer_layer_b200 as H
@@ -357,6 +358,52 @@ def test_touched_rows(R, d, U, cap, bits):
     np.testing.assert_array_equal(t["v_scale"].cpu().numpy()[at], sr)
     others = np.setdiff1d(np.arange(R * nb), at)
     assert torch.equal(t["m_scale"][others], old["m_scale"][others])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_tables_of_all_types_in_one_list(bits):
+    """Touched rows of tables with and without masters: the bits that a dense
+    step gives these rows (with rows of 512 the blocks of 256 are the same)."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    R, d, U = 700, 512, 260
+    types = [("bf16", "f32", False), ("bf16", "bf16", False), ("f32", "f32", False),
+             ("bf16", "f32", True), ("f16", "f32", False)]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    sparse, dense, rows = [], [], []
+    for i, (p, g, master) in enumerate(types):
+        t = _make(0, p, g, master, bits, 10 + i, shape=(R, d))
+        dense.append(_copy(t))
+        ids = torch.randperm(R, device="cuda", generator=gen)[:U].sort().values
+        t["grad"], t["row_ids"] = t["grad"][ids].contiguous(), ids
+        t["n_rows"] = torch.tensor([U], device="cuda")
+        sparse.append(t)
+        rows.append(ids)
+    ws = _ws(256)
+    for ts in (sparse, dense):
+        H.hstu_adamw_step(H.AdamWTensors(ts), ws, step=3, seed=2, **HYPER)
+        assert H.hstu_read_status(ws) == 0
+    for t, o, ids in zip(sparse, dense, rows):
+        for k in ("param", "master", "m", "v"):
+            if k in t:
+                assert torch.equal(t[k].view(R, d)[ids].view(torch.uint8), o[k].view(R, d)[ids].view(torch.uint8))
+        if bits == 8:
+            for k in ("m_scale", "v_scale"):
+                assert torch.equal(t[k].view(R, 2)[ids], o[k].view(R, 2)[ids])
+
+
+@pytest.mark.parametrize("n", [0, 2])
+def test_row_count_of_another_size_is_refused(n):
+    """An empty count has a null address, which would mean a dense gradient."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    t = _make(0, "f32", "f32", False, 32, 1, shape=(10, 16))
+    t["row_ids"] = torch.arange(10, device="cuda")
+    t["n_rows"] = torch.zeros(n, dtype=torch.int64, device="cuda")
+    with pytest.raises(H.HstuError):
+        H.AdamWTensors([t])
+    with pytest.raises(H.HstuError):
+        H.GradTensors([dict(grad=t["grad"], n_rows=t["n_rows"])])
 
 
 @pytest.mark.parametrize("bits,d", [(32, 16), (8, 16), (8, 512), (32, 512), (8, 7)])
