@@ -156,8 +156,9 @@ constexpr int kLookupUnroll = 4;
 constexpr int64_t kCheckMax = 65536;
 
 // Y[t] = scale * E[ids[t]].  Bandwidth-bound (19.7 us for 38,070 x 1024 bf16:
-// 78 MB written and the touched rows read, at 4.6 TB/s; setting 78 MB to zero
-// takes 20.7); a thread keeps one column group of 8 elements (1 where a row is
+// 78 MB written and the touched rows read, at 4.6 TB/s; only setting 78 MB to
+// zero takes 12.2; more loads ahead, places of rows in shared memory and other
+// numbers of blocks gave 18.9 to 26); a thread keeps one column group of 8 elements (1 where a row is
 // not a multiple of 8) and walks the tokens, 4 loads in flight, so that no index
 // is divided inside the loop.
 // Both types are compiled in: with a branch on the output's type per store the
@@ -1047,24 +1048,27 @@ cudaError_t sort_tokens_cluster(const SortArgs& a, const FillArgs& f, cudaStream
   *done = false;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(k_embed_sort), (int)smem);
   if (e != cudaSuccess) return e;
-  int fill = 0;  // clusters that clear and ask, 64 KB or more for each of their blocks
-  if (f.out || f.ask) {
-    const int64_t bytes = (f.out ? f.rows * f.row_bytes : 0) + f.ask_bytes;
-    fill = (int)std::min<int64_t>((bytes + 65535) / 65536 / nc + 1, num_sms() / nc - 1);
-    fill = std::max(fill, 1);
-  }
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)nc;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(nc * (1 + fill)));
+  cfg.gridDim = dim3((unsigned)nc);
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (!cluster_fits(reinterpret_cast<const void*>(k_embed_sort), nc, cfg)) return cudaSuccess;
+  const int resident = clusters_resident(reinterpret_cast<const void*>(k_embed_sort), nc, cfg);
+  if (resident == 0) return cudaSuccess;
+  if (f.out || f.ask) {
+    // clusters that clear and ask: 64 KB or more for each of their blocks, and no more than run at
+    // once beside the sort (clusters of 16 lie within a GPC: one more than that waited for the
+    // first to end, and the dense gradient of 65,536 x 512 took 67 us instead of 57)
+    const int64_t bytes = (f.out ? f.rows * f.row_bytes : 0) + f.ask_bytes;
+    const int64_t fill = std::min<int64_t>((bytes + 65535) / 65536 / nc + 1, resident - 1);
+    cfg.gridDim.x = (unsigned)(nc * (1 + std::max<int64_t>(fill, 1)));
+  }
   *done = true;
   LaunchScope ls(K_EMBED_SORT, s);
   return cudaLaunchKernelEx(&cfg, k_embed_sort, a, f, tile);

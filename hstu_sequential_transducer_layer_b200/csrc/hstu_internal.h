@@ -78,10 +78,10 @@ int num_sms();
 // Raises `fn`'s dynamic shared-memory limit to at least `bytes` on the
 // current device (again only when a larger limit is needed).
 cudaError_t ensure_smem_limit(const void* fn, int bytes);
-// Whether clusters of `blocks` blocks (up to 16, more than 8 being opt-in) fit
-// the current device with this launch's block size and shared memory; asked
-// once per device, kernel, size and amount.
-bool cluster_fits(const void* fn, int blocks, const cudaLaunchConfig_t& cfg);
+// How many clusters of `blocks` blocks (up to 16, more than 8 being opt-in) the
+// current device runs at once with this launch's block size and shared memory
+// (0: it cannot run them); asked once per device, kernel, size and amount.
+int clusters_resident(const void* fn, int blocks, const cudaLaunchConfig_t& cfg);
 // Bound of an in-kernel wait unless a test asks for a shorter one.
 constexpr uint32_t kDefaultWaitLimitUs = 1000u * 1000u;
 // The wait bound and stall injection for the next attention launch

@@ -975,7 +975,7 @@ hstu_status grad_norm(const hstu_adamw_tensor* tensors, int n_tensors, double ma
       at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3(kNormCluster);
       cfg.blockDim = dim3(kNormThreads * kNormGroups);
-      if (cluster_fits(reinterpret_cast<const void*>(k_norm_small<N>), kNormCluster, cfg))
+      if (clusters_resident(reinterpret_cast<const void*>(k_norm_small<N>), kNormCluster, cfg) > 0)
         return cuda_status(cudaLaunchKernelEx(&cfg, k_norm_small<N>, a), "hstu_grad_norm");
     }
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(a.chunks, most));

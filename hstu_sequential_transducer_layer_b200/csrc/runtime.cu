@@ -72,11 +72,11 @@ cudaError_t ensure_smem_limit(const void* fn, int bytes) {
   return e;
 }
 
-bool cluster_fits(const void* fn, int blocks, const cudaLaunchConfig_t& cfg) {
+int clusters_resident(const void* fn, int blocks, const cudaLaunchConfig_t& cfg) {
   static std::mutex mu;
-  static std::map<std::tuple<const void*, int, int, size_t>, bool> known;
+  static std::map<std::tuple<const void*, int, int, size_t>, int> known;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   std::lock_guard<std::mutex> lk(mu);
   const auto key = std::make_tuple(fn, dev, blocks, cfg.dynamicSmemBytes);
   const auto it = known.find(key);
@@ -86,8 +86,7 @@ bool cluster_fits(const void* fn, int blocks, const cudaLaunchConfig_t& cfg) {
       cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
       cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
   if (!ok) cudaGetLastError();
-  known[key] = ok;
-  return ok;
+  return known[key] = ok ? n : 0;
 }
 
 // ---------------------------------------------------------------- wait test hook
