@@ -132,9 +132,11 @@ DEVI double sum_chunks(const NormArgs<N>& a, int64_t group, int64_t groups) {
       int64_t n = q.n;
       if (q.n_rows) n = min(max(*q.n_rows, (int64_t)0), q.max_rows) * q.row_len;
       const int64_t e0 = (c - q.chunk0) * kNormChunk;
-      const int m = in ? (int)min((int64_t)kNormChunk, n - e0) : 0;  // may be <= 0
+      // elements of this chunk that count; none behind a row-sparse gradient's rows in use, which
+      // may lie more than 2^31 elements before the chunk
+      const int m = in && e0 < n ? (int)min((int64_t)kNormChunk, n - e0) : 0;
       const int per = dtype[k] == HSTU_FP32 ? 4 : 8;
-      const int vecs = m > 0 ? m / per : 0;
+      const int vecs = m / per;
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const uint8_t*>(q.grad) + e0 * (dtype[k] == HSTU_FP32 ? 4 : 2));
 #pragma unroll

@@ -584,3 +584,22 @@ def test_offsets_past_32_bits():
     for r in (0, R - 2, R - 1):
         assert (t["param"][r] == want).all() and (t["m_scale"][4 * r:4 * r + 4] > 0).all()
     assert not t["param"][1:R - 2].any() and not t["m"][1:R - 2].any()
+
+
+def test_norm_of_few_rows_in_a_large_buffer():
+    """Rows in use at the start of a buffer of more than 2^31 elements: what lies behind them does not
+    count, however far behind; with every row in use all of it does."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    R, d = 2_200_000, 1024
+    rows = torch.full((R, d), 2.0, dtype=torch.bfloat16, device="cuda")
+    n = torch.zeros(1, dtype=torch.int64, device="cuda")
+    lst = H.GradTensors([dict(grad=rows, n_rows=n), dict(grad=torch.full((9,), 2.0, device="cuda"))])
+    out, ws = torch.zeros(2, device="cuda"), _ws(H.hstu_grad_norm_workspace_size())
+    for k in (0, 1, 100, R - 1, R):
+        n.fill_(k)
+        H.hstu_grad_norm(lst, 1.0, out, ws)
+        want = 2.0 * math.sqrt(k * d + 9)          # every square and sum is exact
+        assert H.hstu_read_status(ws) == 0
+        assert abs(float(out[0]) - want) <= 1.01 * E * want
+        assert abs(float(out[1]) - 1 / want) <= 1.01 * E / want
