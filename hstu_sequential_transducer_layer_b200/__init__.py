@@ -18,7 +18,8 @@ from .binding import (  # noqa: F401
     hstu_set_option, hstu_debug_keep_z, hstu_debug_wait_test,
     hstu_sl_embed_ids, hstu_embed_workspace_size, hstu_embed_fwd, hstu_embed_bwd_workspace_size,
     hstu_embed_bwd, hstu_embed_bwd_rows, GradTensors, AdamWTensors, state_scales,
-    hstu_grad_norm_workspace_size, hstu_grad_norm, hstu_adamw_workspace_size, hstu_adamw_step,
+    hstu_grad_norm_workspace_size, hstu_grad_norm, hstu_grad_norm_after,
+    hstu_adamw_workspace_size, hstu_adamw_step,
 )
 from .runner import HSTURunner, TransformerRunner  # noqa: F401,E402
 from .trainer import HSTUTrainer  # noqa: F401,E402

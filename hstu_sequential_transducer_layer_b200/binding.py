@@ -29,8 +29,8 @@ EXPORTED = ["hstu_workspace_size", "hstu_layer_fwd", "hstu_stack_fwd", "hstu_mfa
             "hstu_layer_fwd_noalloc", "hstu_sl_embed_workspace_size", "hstu_sl_embed",
             "hstu_sl_embed_ids", "hstu_embed_workspace_size", "hstu_embed_fwd",
             "hstu_embed_bwd_workspace_size", "hstu_embed_bwd", "hstu_embed_bwd_rows",
-            "hstu_grad_norm_workspace_size", "hstu_grad_norm", "hstu_adamw_workspace_size",
-            "hstu_adamw_step",
+            "hstu_grad_norm_workspace_size", "hstu_grad_norm", "hstu_grad_norm_after",
+            "hstu_adamw_workspace_size", "hstu_adamw_step",
             "hstu_sl_keep_count", "hstu_bf16_to_f16", "hstu_retrieval_workspace_size",
             "hstu_retrieval_topk", "hstu_retrieval_fallback_taken",
             "hstu_transformer_workspace_size",
@@ -172,6 +172,8 @@ def lib() -> ctypes.CDLL:
     L.hstu_embed_bwd_rows.restype = i32
     L.hstu_grad_norm.argtypes = [pt, i32, ctypes.c_double, vp, vp, sz, vp]
     L.hstu_grad_norm.restype = i32
+    L.hstu_grad_norm_after.argtypes = [pt, i32, ctypes.c_double, vp, vp, vp, sz, vp]
+    L.hstu_grad_norm_after.restype = i32
     L.hstu_adamw_step.argtypes = [vp, pt, i32, vp, sz, vp]  # hstu_adamw_args, packed or by address
     L.hstu_adamw_step.restype = i32
     L.hstu_read_status.argtypes = [vp, sz, vp]
@@ -625,15 +627,34 @@ def hstu_grad_norm(tensors: GradTensors, max_norm: float, out, workspace, stream
     """out (fp32 [2]): the norm over all gradients, and the factor that clips it
     to max_norm (NaN if the norm is not finite); see include/hstu.h."""
     w = "hstu_grad_norm"
-    dev = _here(w, out, workspace)
-    if tensors.device is not None and tensors.device != dev:
-        raise HstuError(1, f"{w}: the tensors are on another device")
-    if out.dtype != _FP32 or not out.is_contiguous() or out.numel() < 2:
-        raise HstuError(1, f"{w}: out: fp32 [2]")
+    dev = _norm_args(w, tensors, out, workspace)
     code = lib().hstu_grad_norm(tensors.array, tensors.n, max_norm, out.data_ptr(),
                                 workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, dev))
     if code != 0:
         _check(code, w)
+
+
+def hstu_grad_norm_after(tensors: GradTensors, max_norm: float, after, out, workspace,
+                         stream=None) -> None:
+    """hstu_grad_norm of gradients that the call with the workspace `after`
+    made: NaN, NaN if that call failed on the device (see include/hstu.h)."""
+    w = "hstu_grad_norm_after"
+    dev = _norm_args(w, tensors, out, workspace, after)
+    _need(_nbytes(after) >= 4, w, "after: a workspace")
+    code = lib().hstu_grad_norm_after(tensors.array, tensors.n, max_norm, after.data_ptr(),
+                                      out.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+                                      _raw_stream(stream, dev))
+    if code != 0:
+        _check(code, w)
+
+
+def _norm_args(w: str, tensors: GradTensors, out, *workspaces) -> int:
+    dev = _here(w, out, *workspaces)
+    if tensors.device is not None and tensors.device != dev:
+        raise HstuError(1, f"{w}: the tensors are on another device")
+    if out.dtype != _FP32 or not out.is_contiguous() or out.numel() < 2:
+        raise HstuError(1, f"{w}: out: fp32 [2]")
+    return dev
 
 
 def hstu_adamw_workspace_size() -> int:

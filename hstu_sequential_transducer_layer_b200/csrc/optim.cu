@@ -46,8 +46,9 @@ struct NormArgs {
   int64_t chunks;
   double* part;  // [gridDim.x]
   int* status;
-  double max_norm;  // one-launch form only, with out
+  double max_norm;  // one-launch form only, with out and after
   float* out;
+  const int* after;
 };
 
 struct NormFinal {
@@ -55,6 +56,7 @@ struct NormFinal {
   int parts;
   double max_norm;
   float* out;
+  const int* after;  // status word of the call that made the gradients, or null
 };
 
 DEVI void add_squares(double& acc, int dtype, const uint4& r) {
@@ -95,8 +97,9 @@ DEVI double block_sum(double x, double* s_warp) {
   return sum;
 }
 
-DEVI void write_norm(double sum, double max_norm, float* out) {
-  const float norm = (float)sqrt(sum);
+DEVI void write_norm(double sum, double max_norm, float* out, const int* after) {
+  // a failed call left its gradients unwritten, or partly written: whatever they add up to, no norm
+  const float norm = after && *after != HSTU_OK ? __int_as_float(0x7fffffff) : (float)sqrt(sum);
   out[0] = norm;
   // not finite: NaN, which makes the AdamW step leave everything as it is
   out[1] = !(norm <= 3.402823466e38f) ? __int_as_float(0x7fffffff)
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(1024) k_norm_final(const NormFinal a) {
   double x = 0;
   for (int i = threadIdx.x; i < a.parts; i += blockDim.x) x += a.part[i];
   const double sum = block_sum(x, s_warp);
-  if (threadIdx.x == 0) write_norm(sum, a.max_norm, a.out);
+  if (threadIdx.x == 0) write_norm(sum, a.max_norm, a.out, a.after);
 }
 
 // The whole norm in one launch, by one cluster of 16 blocks, where that is
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kNormThreads * kNormGroups)
 #pragma unroll
     for (int r = 0; r < kNormCluster; ++r) all += __shfl_sync(0xffffffffu, x, r);
     if (threadIdx.x == 0) {
-      write_norm(all, a.max_norm, a.out);
+      write_norm(all, a.max_norm, a.out, a.after);
       *a.status = HSTU_OK;
     }
   }
@@ -936,8 +939,8 @@ constexpr int kNormMaxParts = 148 * kNormBlocksPerSm * 8;
 constexpr int64_t kNormSmallChunks = 256;  // of 4096 elements
 
 template <int N>
-hstu_status grad_norm(const hstu_adamw_tensor* tensors, int n_tensors, double max_norm, float* out,
-                      void* ws, cudaStream_t s) {
+hstu_status grad_norm(const hstu_adamw_tensor* tensors, int n_tensors, double max_norm,
+                      const int* after, float* out, void* ws, cudaStream_t s) {
   double* part = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 256);
   const int launches = std::max(1, (n_tensors + N - 1) / N);
   const int most = std::min(num_sms() * kNormBlocksPerSm, kNormMaxParts / launches);
@@ -969,6 +972,7 @@ hstu_status grad_norm(const hstu_adamw_tensor* tensors, int n_tensors, double ma
     a.status = static_cast<int*>(ws);
     a.max_norm = max_norm;
     a.out = out;
+    a.after = after;
     LaunchScope ls(K_GRAD_NORM, s);
     cudaError_t e;
     if (launches == 1 && a.chunks <= kNormSmallChunks) {
@@ -986,7 +990,7 @@ hstu_status grad_norm(const hstu_adamw_tensor* tensors, int n_tensors, double ma
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_status(e, "hstu_grad_norm");
   }
-  NormFinal f{part, parts, max_norm, out};
+  NormFinal f{part, parts, max_norm, out, after};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(1);
@@ -1079,10 +1083,13 @@ extern "C" {
 
 size_t hstu_grad_norm_workspace_size(void) { return 256 + (size_t)hstu::kNormMaxParts * 8; }
 
-hstu_status hstu_grad_norm(const hstu_adamw_tensor* tensors, int32_t n_tensors, double max_norm,
-                           float* out, void* ws, size_t ws_bytes, void* stream) {
+hstu_status hstu_grad_norm_after(const hstu_adamw_tensor* tensors, int32_t n_tensors,
+                                 double max_norm, const void* after, float* out, void* ws,
+                                 size_t ws_bytes, void* stream) {
   using namespace hstu;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int* word = static_cast<const int*>(after);
+  if (!al256(after)) return HSTU_ERR_INVALID_ARG;
   if (n_tensors < 0 || (n_tensors > 0 && !tensors) || !out || !al16(out) || !(max_norm > 0))
     return HSTU_ERR_INVALID_ARG;
   if (n_tensors > HSTU_MAX_TENSORS) return HSTU_ERR_UNSUPPORTED;
@@ -1091,8 +1098,13 @@ hstu_status hstu_grad_norm(const hstu_adamw_tensor* tensors, int32_t n_tensors, 
     if (!grad_ok(tensors[i], &sparse)) return HSTU_ERR_INVALID_ARG;
   if (!ws || ws_bytes < hstu_grad_norm_workspace_size() || !al256(ws)) return HSTU_ERR_WORKSPACE;
   return n_tensors <= kFewTensors
-             ? grad_norm<kFewTensors>(tensors, n_tensors, max_norm, out, ws, s)
-             : grad_norm<kMaxTensors>(tensors, n_tensors, max_norm, out, ws, s);
+             ? grad_norm<kFewTensors>(tensors, n_tensors, max_norm, word, out, ws, s)
+             : grad_norm<kMaxTensors>(tensors, n_tensors, max_norm, word, out, ws, s);
+}
+
+hstu_status hstu_grad_norm(const hstu_adamw_tensor* tensors, int32_t n_tensors, double max_norm,
+                           float* out, void* ws, size_t ws_bytes, void* stream) {
+  return hstu_grad_norm_after(tensors, n_tensors, max_norm, nullptr, out, ws, ws_bytes, stream);
 }
 
 size_t hstu_adamw_workspace_size(void) { return 256; }

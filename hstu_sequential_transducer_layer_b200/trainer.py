@@ -82,7 +82,9 @@ class HSTUTrainer:
         which was looked up with the factor `embed_scale`.  `lr`: this step's
         rate (default: the constructor's).  Returns dX; `norm` holds the
         gradient norm and the clip factor.  A step whose gradients are not all
-        finite (clip factor NaN) changes nothing, but is counted in `steps`."""
+        finite, or whose backward pass failed on the device (a bad batch;
+        status() tells), has a clip factor of NaN and changes nothing, but is
+        counted in `steps`; dX is not written by a failed pass."""
         if (ids is None) != (self.table is None):
             raise _b.HstuError(1, "HSTUTrainer.step: ids and a table come together")
         if ids is not None and ids.numel() > self.max_tokens:
@@ -93,7 +95,8 @@ class HSTUTrainer:
             _b.hstu_embed_bwd_rows(ids, dX, self.table.shape[0], self.row_ids, self.row_grad,
                                    self.n_rows, self._ews, scale=embed_scale, pad_id=pad_id,
                                    stream=stream)
-        _b.hstu_grad_norm(self.list, self.max_norm, self.norm, self._nws, stream=stream)
+        _b.hstu_grad_norm_after(self.list, self.max_norm, self.runner._bws, self.norm, self._nws,
+                                stream=stream)
         self.steps += 1
         _b.hstu_adamw_step(self.list, self._ows, lr=self.lr if lr is None else lr,
                            step=self.steps, beta1=self.betas[0], beta2=self.betas[1],

@@ -484,6 +484,14 @@ typedef struct {
 size_t hstu_grad_norm_workspace_size(void);
 hstu_status hstu_grad_norm(const hstu_adamw_tensor* tensors, int32_t n_tensors, double max_norm,
                            float* out, void* workspace, size_t workspace_bytes, void* stream);
+/* hstu_grad_norm of gradients that an earlier call on the stream made:
+ * `after` is that call's workspace (hstu_layer_bwd, hstu_stack_bwd; null: as
+ * hstu_grad_norm).  If its status word is not HSTU_OK, the gradients were not
+ * (all) written, and out[0] and out[1] are NaN, so that an AdamW step with
+ * out[1] as its grad_scale changes nothing. */
+hstu_status hstu_grad_norm_after(const hstu_adamw_tensor* tensors, int32_t n_tensors,
+                                 double max_norm, const void* after, float* out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 /* One AdamW step (decoupled weight decay) of a list of tensors.  With
  * g = grad_scale * grad and t = step, per element

@@ -603,3 +603,26 @@ def test_norm_of_few_rows_in_a_large_buffer():
         assert H.hstu_read_status(ws) == 0
         assert abs(float(out[0]) - want) <= 1.01 * E * want
         assert abs(float(out[1]) - 1 / want) <= 1.01 * E / want
+
+
+@pytest.mark.parametrize("n", [0, 1000, 2_000_000])
+def test_norm_after_a_failed_call_is_nan(n):
+    """In one launch and in two, and with nothing to add up: any status word but HSTU_OK gives NaN, and
+    the AdamW step behind it changes nothing."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    t = _make(n, "bf16", "f32", True, 32, 1)
+    old, lst = _copy(t), H.AdamWTensors([t] if n else [])
+    out, ws, ows = torch.zeros(2, device="cuda"), _ws(H.hstu_grad_norm_workspace_size()), _ws(256)
+    after = torch.zeros(64, dtype=torch.int32, device="cuda")
+    for word in (5, 6, 7, -1):
+        after[0] = word
+        H.hstu_grad_norm_after(lst, 1.0, after, out, ws)
+        assert torch.isnan(out).all() and H.hstu_read_status(ws) == 0
+        H.hstu_adamw_step(lst, ows, step=1, grad_scale=out[1:], **HYPER)
+        assert all(torch.equal(t[k], x) for k, x in old.items())
+    after[0], after[1:] = 0, 9                     # the rest of a workspace means nothing
+    H.hstu_grad_norm_after(lst, 1.0, after, out, ws)
+    plain = torch.zeros(2, device="cuda")
+    H.hstu_grad_norm(lst, 1.0, plain, ws)
+    assert torch.equal(out, plain) and torch.isfinite(out).all()

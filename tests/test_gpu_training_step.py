@@ -169,3 +169,39 @@ def test_trainer_without_a_table():
     assert tr.status() == 0
     for t in tr.tensors:
         assert torch.isfinite(t["param"]).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_failed_backward_pass_changes_nothing(bits):
+    """A batch with a user whose timestamps span more than the stack takes, and one whose offsets do not
+    end at its rows, as the first step and behind a good one: weights, masters, copies, states and table
+    stay as they are, status() tells why, and the next good step runs."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    dims = hw.LayerDims(128, 2, 64, 64, 64, 128, 3, 2, 1e-6, hw.BF16)
+    w = hw.custom("failed", [60, 7, 33], dims, n_layers=2, seed=5)
+    r = runner_for(w)
+    table = torch.randn(40, 128, device="cuda").to(torch.bfloat16)
+    tr = H.HSTUTrainer(r, table, max_tokens=100, state_bits=bits, lr=1e-2, table_decay=0.1)
+    off, ts, X = r.to_device(w.offsets, "i64"), r.to_device(w.timestamps, "i64"), r.to_device(w.X)
+    dY = torch.randn(100, 128, device="cuda").to(torch.bfloat16)
+    ids = torch.arange(100, device="cuda") % 37
+    late, short = ts.clone(), off.clone()
+    late[5] += 1 << 31
+    short[-1] -= 1
+    keep = lambda: [{q: x.clone() for q, x in t.items() if hasattr(x, "clone")}  # noqa: E731
+                    for t in tr.tensors]
+
+    def same(old):
+        return [all(torch.equal(t[q].view(torch.uint8), o[q].view(torch.uint8)) for q in o
+                    if q not in ("grad", "row_ids", "n_rows")) for t, o in zip(tr.tensors, old)]
+    for k in range(2):
+        for o, t, want in ((off, late, 7), (short, ts, 5)):
+            old = keep()
+            tr.step(o, X, t, dY, w.max_len, ids=ids)
+            assert tr.status() == want
+            assert all(same(old)) and torch.isnan(tr.norm).all()
+        old = keep()
+        tr.step(off, X, ts, dY, w.max_len, ids=ids)
+        assert tr.status() == 0 and torch.isfinite(tr.norm).all()
+        assert not any(same(old))

@@ -213,3 +213,16 @@ def test_binding_refuses_host_tensors():
         H.hstu_embed_fwd(ids, tab, out, ws)
     with pytest.raises(B.HstuError):
         H.GradTensors([dict(grad=torch.zeros(4))])
+
+
+def test_norm_after_refusals():
+    L = B.lib()
+    n0 = H.hstu_launch_count()
+    wn = L.hstu_grad_norm_workspace_size()
+    norm = lambda after=0x20000, n=1, mx=1.0, out=0x8000, w=0x10000, wb=wn: L.hstu_grad_norm_after(
+        ctypes.byref(_tensor()), n, mx, after, out, w, wb, None)
+    for bad in (dict(after=0x20010), dict(after=4), dict(n=-1), dict(mx=0.0), dict(out=None),
+                dict(out=0x8004)):
+        assert norm(**bad) == 1, bad
+    assert norm(wb=wn - 1) == 3 and norm(w=None) == 3 and norm(n=5000) == 2
+    assert H.hstu_launch_count() == n0
