@@ -444,6 +444,15 @@ def _here(where: str, *tensors) -> int:
     return dev
 
 
+def stream_handle(stream) -> int:
+    """The integer handle of `stream` (None: the current one)."""
+    if stream is not None:
+        return _stream(stream)
+    if _DTYPES is None:
+        _torch_names()
+    return _current_raw_stream(_current_device())
+
+
 def _raw_stream(stream, dev: int) -> int:
     return _current_raw_stream(dev) if stream is None else _stream(stream)
 

@@ -1,13 +1,53 @@
 """Holds a layer descriptor, device weights and a reusable workspace, and
 calls the C ABI with them.  Allocation (weights, workspace, outputs) goes
-through torch; the computation is the library's."""
+through torch; the computation is the library's.
+
+A call runs on `stream` (a torch stream or its integer handle), or on torch's
+current stream.  What the call allocates belongs to the stream it runs on, so
+memory that is given back (a workspace that has to grow, an output that the
+caller drops) is not handed out while that call still uses it.  The calls of
+one object share its workspace: on several streams the caller orders them."""
 from __future__ import annotations
 
+from contextlib import nullcontext
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
 
 from . import binding as _b
+
+
+def _torch_stream(stream):
+    import torch
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+
+
+def _made_on(stream):
+    """Context whose allocations belong to `stream` (None: the current one)."""
+    if stream is None:
+        return nullcontext()
+    import torch
+    return torch.cuda.stream(_torch_stream(stream))
+
+
+class _Buffers:
+    """Buffers kept between calls, with the streams that they were used on: a
+    buffer that is replaced goes back to the allocator only when all of those
+    are through with it."""
+
+    def __init__(self):
+        self.used = {}  # name -> handles of streams
+
+    def use(self, name: str, stream) -> None:
+        self.used.setdefault(name, set()).add(_b.stream_handle(stream))
+
+    def replace(self, name: str, *old) -> None:
+        for h in self.used.pop(name, ()):
+            for t in old:
+                if t is not None:
+                    t.record_stream(_torch_stream(h))
 
 
 class HSTURunner:
@@ -34,13 +74,21 @@ class HSTURunner:
                                                 device=self.device)
                     _b.hstu_bf16_to_f16(w[k], w[k + "_f16"])
         self._warr = _b.weights_array(self.weights)
-        self._ws = None
+        self._ws = self._bws = None
+        self._kept = _Buffers()
 
     # ------------------------------------------------------------ memory
-    def workspace(self, nbytes: int):
-        if self._ws is None or self._ws.numel() < nbytes:
-            self._ws = self.torch.empty(max(nbytes, 256), dtype=self.torch.uint8, device=self.device)
+    def workspace(self, nbytes: int, stream=None):
+        self._ws = self._grown("_ws", self._ws, nbytes, stream)
         return self._ws
+
+    def _grown(self, name: str, ws, nbytes: int, stream):
+        if ws is None or ws.numel() < nbytes:
+            self._kept.replace(name, ws)
+            with _made_on(stream):
+                ws = self.torch.empty(max(nbytes, 256), dtype=self.torch.uint8, device=self.device)
+        self._kept.use(name, stream)
+        return ws
 
     def to_device(self, a: np.ndarray, kind: str = "act"):
         t = self.torch
@@ -58,9 +106,10 @@ class HSTURunner:
         B = offsets.numel() - 1
         T = X.shape[0]
         if out is None:
-            out = self.torch.empty_like(X)
+            with _made_on(stream):
+                out = self.torch.empty_like(X)
         nb = _b.hstu_workspace_size(self.desc, L, B, T, max_len)
-        ws = self.workspace(nb)
+        ws = self.workspace(nb, stream)
         if L == 1:
             _b.hstu_layer_fwd(self.desc, B, T, max_len, offsets, X, self._warr[0], timestamps, out,
                               ws, stream)
@@ -92,17 +141,22 @@ class HSTURunner:
         d = int(content_table.shape[1])
         key = (B, T, d)
         if getattr(self, "_sl_key", None) != key:
+            if hasattr(self, "_sl_key"):
+                self._kept.replace("_sl", self._sl_off, self._sl_X, self._sl_ts, self._sl_ws)
             self._sl_key = key
-            self._sl_off = t.empty(B + 1, dtype=t.int64, device=self.device)
-            self._sl_X = t.empty(max(T, 1), d, dtype=t.bfloat16, device=self.device)
-            self._sl_ts = t.empty(max(T, 1), dtype=t.int64, device=self.device)
-            self._sl_ws = t.empty(_b.hstu_sl_embed_workspace_size(), dtype=t.uint8,
-                                  device=self.device)
+            with _made_on(stream):
+                self._sl_off = t.empty(B + 1, dtype=t.int64, device=self.device)
+                self._sl_X = t.empty(max(T, 1), d, dtype=t.bfloat16, device=self.device)
+                self._sl_ts = t.empty(max(T, 1), dtype=t.int64, device=self.device)
+                self._sl_ws = t.empty(_b.hstu_sl_embed_workspace_size(), dtype=t.uint8,
+                                      device=self.device)
+        self._kept.use("_sl", stream)
         _b.hstu_sl_embed(B, R, max_raw_len, raw_offsets, raw_ids, raw_ts, seed, content_table,
                          action_table, self._sl_off, self._sl_X, self._sl_ts, self._sl_ws, stream)
         X = self._sl_X[:T]
         if out is None:
-            out = t.empty_like(X)
+            with _made_on(stream):
+                out = t.empty_like(X)
         self.stack(self._sl_off, X, self._sl_ts[:T], max_len, out=out, stream=stream)
         return out, self._sl_off, self._sl_ts[:T]
 
@@ -115,10 +169,11 @@ class HSTURunner:
         T = history.shape[0]
         C = candidates.shape[0]
         if scores is None:
-            scores = self.torch.empty(C, dtype=self.torch.float32, device=self.device)
+            with _made_on(stream):
+                scores = self.torch.empty(C, dtype=self.torch.float32, device=self.device)
         nb = _b.hstu_workspace_size(self.desc, self.n_layers, B, T, max_len, C, max_cands,
                                     microbatch)
-        ws = self.workspace(nb)
+        ws = self.workspace(nb, stream)
         _b.hstu_mfalcon_rank(self.desc, self.n_layers, self._warr, B, T, max_len, hist_offsets,
                              history, hist_ts, C, max_cands, cand_offsets, candidates, request_ts,
                              microbatch, head_vec, scores, ws, stream)
@@ -141,17 +196,18 @@ class HSTURunner:
         F = 2 * d.n_heads * (d.d_v + d.d_qk)
         hdv = d.n_heads * d.d_v
         if dX is None:
-            dX = t.empty_like(X)
+            with _made_on(stream):
+                dX = t.empty_like(X)
         if grads is None:
             shapes = dict(dW1=(F, d.d_model), db1=(F,), dW2=(d.d_model, hdv), db2=(d.d_model,),
                           dln_gamma=(hdv,), dln_beta=(hdv,),
                           drab_pos=(d.n_heads, d.n_pos_buckets),
                           drab_time=(d.n_heads, d.n_time_buckets))
-            grads = [{k: t.empty(v, dtype=t.float32, device=self.device) for k, v in shapes.items()}
-                     for _ in range(L)]
+            with _made_on(stream):
+                grads = [{k: t.empty(v, dtype=t.float32, device=self.device)
+                          for k, v in shapes.items()} for _ in range(L)]
         nb = _b.hstu_bwd_workspace_size(self.desc, L, B, T, max_len)
-        if getattr(self, "_bws", None) is None or self._bws.numel() < nb:
-            self._bws = t.empty(max(nb, 256), dtype=t.uint8, device=self.device)
+        self._bws = self._grown("_bws", self._bws, nb, stream)
         if L == 1:
             _b.hstu_layer_bwd(self.desc, self._warr[0], B, T, max_len, offsets, X, timestamps, dY,
                               dX, grads, self._bws, stream)
@@ -207,16 +263,21 @@ class TransformerRunner:
         self._struct = _b.TransformerWeights(*[_b._ptr(self.w[k]) for k, _ in
                                                _b.TransformerWeights._fields_])
         self._ws = None
+        self._kept = _Buffers()
 
     def layer(self, offsets, X, max_len: int, out=None, stream=None):
         t = self.torch
         B = offsets.numel() - 1
         T = X.shape[0]
         if out is None:
-            out = t.empty_like(X)
+            with _made_on(stream):
+                out = t.empty_like(X)
         nb = _b.hstu_transformer_workspace_size(self.d, self.h, self.ff, B, T)
         if self._ws is None or self._ws.numel() < nb:
-            self._ws = t.empty(nb, dtype=t.uint8, device=self.device)
+            self._kept.replace("_ws", self._ws)
+            with _made_on(stream):
+                self._ws = t.empty(nb, dtype=t.uint8, device=self.device)
+        self._kept.use("_ws", stream)
         _b.hstu_transformer_layer_fwd(self.d, self.h, self.ff, self.eps, self._struct, B, T,
                                       max_len, offsets, X, out, self._ws, stream)
         return out

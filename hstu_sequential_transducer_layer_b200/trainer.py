@@ -23,7 +23,10 @@ class HSTUTrainer:
     W1 and W2 the update writes them too, so the next forward needs no
     conversion.  `table`: device [rows, d_model] (for hstu_sl_embed_ids: the
     content rows, then the action rows); at most `max_tokens` tokens per step.
-    Only the rows that a step's tokens touch are updated."""
+    Only the rows that a step's tokens touch are updated.
+
+    The state is made on torch's current stream; a step on another stream has
+    to be ordered behind that (`stream.wait_stream`), as for its inputs."""
 
     def __init__(self, runner: HSTURunner, table=None, max_tokens: int = 0, state_bits: int = 32,
                  lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,

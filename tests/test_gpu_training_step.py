@@ -205,3 +205,69 @@ def test_a_failed_backward_pass_changes_nothing(bits):
         tr.step(off, X, ts, dY, w.max_len, ids=ids)
         assert tr.status() == 0 and torch.isfinite(tr.norm).all()
         assert not any(same(old))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_steps_on_a_stream_of_their_own(handle):
+    """Two steps queued behind a pause of another stream, the second on a batch that makes the workspace
+    grow, dX dropped each time: what the current stream allocates meanwhile, of those very sizes, is not
+    written by them, and the weights are those of the same steps on the current stream."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    dims = hw.LayerDims(128, 2, 64, 64, 64, 128, 3, 2, 1e-6, hw.BF16)
+    batches = [hw.custom("streams", n, dims, n_layers=2, seed=9) for n in ([60, 7, 33], [260, 301, 40])]
+    runners = [runner_for(batches[0]) for _ in range(2)]
+    trainers = [H.HSTUTrainer(r, torch.ones(50, 128, dtype=torch.bfloat16, device="cuda"), max_tokens=601)
+                for r in runners]
+    inputs = [(runners[0].to_device(w.offsets, "i64"), runners[0].to_device(w.X),
+               runners[0].to_device(w.timestamps, "i64"), runners[0].to_device(w.X[::-1]), w.max_len,
+               torch.arange(w.T, device="cuda") % 50) for w in batches]
+    for off, X, ts, dY, longest, ids in inputs:
+        trainers[0].step(off, X, ts, dY, longest, ids=ids)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for r, tr in ((runners[1], trainers[1]),):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)               # cycles: a tenth of a second
+        sizes = []
+        for off, X, ts, dY, longest, ids in inputs:
+            tr.step(off, X, ts, dY, longest, ids=ids, stream=side.cuda_stream if handle else side)
+            sizes += [X.numel() * 2, r._bws.numel()]
+        paused = not side.query()
+        others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    torch.cuda.current_stream().synchronize()
+    assert paused
+    torch.cuda.synchronize()
+    assert all(bool((x == 7).all()) for x in others)
+    assert trainers[1].status(side) == 0
+    for a, b in zip(trainers[0].tensors, trainers[1].tensors):
+        for q in a:
+            if hasattr(a[q], "clone"):
+                assert torch.equal(a[q], b[q]), q
+
+
+def test_outputs_belong_to_the_stream_of_the_call():
+    """The same for the runner's other calls: what they return, once dropped, is not handed to the current
+    stream while the call may still write it."""
+    import torch
+    dims = hw.LayerDims(128, 2, 64, 64, 64, 128, 3, 2, 1e-6, hw.BF16)
+    w = hw.custom("streams", [60, 7, 33], dims, n_layers=2, seed=9)
+    r = runner_for(w)
+    off, X, ts = r.to_device(w.offsets, "i64"), r.to_device(w.X), r.to_device(w.timestamps, "i64")
+    want = r.stack(off, X, ts, w.max_len)
+    torch.cuda.synchronize()
+    r.workspace(0)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    r.stack(off, X, ts, w.max_len, stream=side)                     # dropped
+    r.workspace(r._ws.numel() + 4096)                               # replaced while it is in use
+    got = r.stack(off, X, ts, w.max_len, stream=side)
+    paused = not side.query()
+    others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda")
+              for n in (X.numel() * 2, r._ws.numel() - 4096) for _ in range(4)]
+    torch.cuda.current_stream().synchronize()
+    assert paused
+    torch.cuda.synchronize()
+    assert all(bool((x == 7).all()) for x in others)
+    assert torch.equal(got, want)
