@@ -57,12 +57,16 @@ class HSTUTrainer:
             e = dict(param=table, grad=self.row_grad, row_ids=self.row_ids, n_rows=self.n_rows,
                      weight_decay=table_decay)
             self.tensors.append(self._states(e, (rows, d)))
-            self._ews = t.empty(_b.hstu_embed_bwd_workspace_size(self.max_tokens, rows, d),
-                                dtype=t.uint8, device=dev)
+            self._ews = self._workspace(_b.hstu_embed_bwd_workspace_size(self.max_tokens, rows, d))
         self.list = _b.AdamWTensors(self.tensors)
         self.norm = t.zeros(2, dtype=t.float32, device=dev)
-        self._nws = t.empty(_b.hstu_grad_norm_workspace_size(), dtype=t.uint8, device=dev)
-        self._ows = t.empty(_b.hstu_adamw_workspace_size(), dtype=t.uint8, device=dev)
+        self._nws = self._workspace(_b.hstu_grad_norm_workspace_size())
+        self._ows = self._workspace(_b.hstu_adamw_workspace_size())
+
+    def _workspace(self, nbytes: int):
+        ws = self.torch.empty(nbytes, dtype=self.torch.uint8, device=self.runner.device)
+        ws[:4] = 0  # the status word: HSTU_OK until a call writes it
+        return ws
 
     def _states(self, e, shape):
         t = self.torch
@@ -107,10 +111,11 @@ class HSTUTrainer:
         return dX
 
     def status(self, stream=None) -> int:
-        """The first status that is not HSTU_OK of the last step's calls."""
+        """The first status that is not HSTU_OK of the last step's calls (HSTU_OK
+        before the first one)."""
         for ws in [self.runner._bws] + ([self._ews] if self.table is not None else []) + \
                 [self._nws, self._ows]:
-            s = _b.hstu_read_status(ws, stream)
+            s = 0 if ws is None else _b.hstu_read_status(ws, stream)
             if s != 0:
                 return s
         return 0

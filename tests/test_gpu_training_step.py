@@ -271,3 +271,16 @@ def test_outputs_belong_to_the_stream_of_the_call():
     torch.cuda.synchronize()
     assert all(bool((x == 7).all()) for x in others)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("with_table", [False, True])
+def test_status_before_the_first_step(with_table):
+    """No call has failed yet, whatever the memory of the workspaces held before."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    dims = hw.LayerDims(128, 2, 64, 64, 64, 128, 3, 2, 1e-6, hw.BF16)
+    r = runner_for(hw.custom("fresh", [5], dims, seed=4))
+    for n in (256, 1 << 16, 1 << 20, 1 << 22):              # given back to the allocator at once
+        torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    table = torch.zeros(50, 128, dtype=torch.bfloat16, device="cuda") if with_table else None
+    assert H.HSTUTrainer(r, table, max_tokens=100).status() == 0
