@@ -597,6 +597,10 @@ class AdamWTensors(GradTensors):
             _need(p.dim() == 2 and g.shape[1] == p.shape[1], w, "grad: rows of param")
             c.row_ids = self._take(t["row_ids"], "row_ids")
             c.max_rows = min(g.shape[0], t["row_ids"].numel())
+            if not c.row_ids:
+                # no entries, so no address, which would mean a dense gradient: one that is not read
+                t["no_row_ids"] = torch.zeros(2, dtype=torch.int64, device=p.device)
+                c.row_ids = t["no_row_ids"].data_ptr()
         else:
             _need(g.numel() == p.numel(), w, "grad: the size of param")
         c.n = p.numel()

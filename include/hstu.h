@@ -447,8 +447,9 @@ hstu_status hstu_embed_bwd_rows(int64_t n_tokens, const int64_t* ids, const void
  * embedding table with the gradient of hstu_embed_bwd_rows): the parameter and
  * its states are [n / row_len, row_len], contiguous; `grad` holds up to
  * max_rows rows, of which the first *n_rows belong to the table rows
- * row_ids[0 .. *n_rows), strictly ascending.  Rows without a gradient, their
- * states and the weight decay on them are not touched. */
+ * row_ids[0 .. *n_rows), strictly ascending; row_ids is not null even if
+ * max_rows is 0.  Rows without a gradient, their states and the weight decay
+ * on them are not touched. */
 #define HSTU_STATE_BLOCK 256  /* elements that share a scale in 8-bit states */
 #define HSTU_MAX_TENSORS 4096
 typedef struct {

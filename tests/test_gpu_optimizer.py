@@ -626,3 +626,31 @@ def test_norm_after_a_failed_call_is_nan(n):
     plain = torch.zeros(2, device="cuda")
     H.hstu_grad_norm(lst, 1.0, plain, ws)
     assert torch.equal(out, plain) and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("capacity", [(0, 0), (4, 0), (0, 4)])
+def test_row_list_without_entries(bits, capacity):
+    """A row gradient that has no room for a row (of an empty batch): the table stays as it is, the other
+    tensors of the list are updated, and a count above its room is reported."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    rows, ids = capacity
+    t, dense = _make(0, "bf16", "f32", True, bits, 1, shape=(10, 48)), _make(100, "f32", "f32", False, bits, 2)
+    t["grad"] = torch.full((rows, 48), math.nan, device="cuda")
+    t["row_ids"] = torch.zeros(ids, dtype=torch.int64, device="cuda")
+    t["n_rows"] = torch.zeros(1, dtype=torch.int64, device="cuda")
+    old, old_dense = _copy(t), _copy(dense)
+    lst, ws = H.AdamWTensors([t, dense]), _ws(256)
+    out, nws = torch.zeros(2, device="cuda"), _ws(H.hstu_grad_norm_workspace_size())
+    H.hstu_grad_norm(lst, 1e9, out, nws)
+    want = TR.grad_norm([_np(dense["grad"])], 1e9)[0]
+    assert abs(float(out[0]) - want) <= 1.01 * E * want and float(out[1]) == 1.0
+    H.hstu_adamw_step(lst, ws, step=2, seed=3, **HYPER)
+    assert H.hstu_read_status(ws) == 0
+    assert all(torch.equal(t[k], old[k]) for k in ("param", "master", "m", "v"))
+    _check(old_dense, dense, 2, 1.0, 1, 3, name="f32")
+    t["n_rows"].fill_(1)
+    H.hstu_adamw_step(lst, ws, step=3, seed=3, **HYPER)
+    assert H.hstu_read_status(ws) == BAD_IDS
+    assert all(torch.equal(t[k], old[k]) for k in ("param", "master", "m", "v"))

@@ -284,3 +284,21 @@ def test_status_before_the_first_step(with_table):
         torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
     table = torch.zeros(50, 128, dtype=torch.bfloat16, device="cuda") if with_table else None
     assert H.HSTUTrainer(r, table, max_tokens=100).status() == 0
+
+
+def test_step_of_an_empty_batch():
+    """No tokens: no gradient, so a step without weight decay changes no weight."""
+    import torch
+    import hstu_sequential_transducer_layer_b200 as H
+    dims = hw.LayerDims(128, 2, 64, 64, 64, 128, 3, 2, 1e-6, hw.BF16)
+    r = runner_for(hw.custom("empty", [5], dims, seed=4))
+    table = torch.randn(50, 128, device="cuda").to(torch.bfloat16)
+    tr = H.HSTUTrainer(r, table, max_tokens=10, weight_decay=0.0)
+    old = [t["param"].clone() for t in tr.tensors]
+    z = lambda *s: torch.zeros(*s, dtype=torch.int64, device="cuda")  # noqa: E731
+    X = torch.zeros(0, 128, dtype=torch.bfloat16, device="cuda")
+    for off in (z(1), z(4)):
+        dX = tr.step(off, X, z(0), X, 1, ids=z(0))
+        assert dX.shape == X.shape and tr.status() == 0 and int(tr.n_rows) == 0
+        assert tr.norm.tolist() == [0.0, 1.0]
+    assert all(torch.equal(t["param"], o) for t, o in zip(tr.tensors, old))
