@@ -365,3 +365,23 @@ def test_two_gradients_at_once():
     torch.cuda.synchronize()
     for k in range(2):
         assert torch.equal(g[k], torch.zeros_like(g[k]).index_add_(0, ids[k], dY[k]))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("d,ld", [(40, 40), (40, 48), (41, 43), (512, 520), (1, 9)])
+@pytest.mark.parametrize("T", [1, 900, 9001])
+def test_touched_rows_output_types_and_strides(T, d, ld, out):
+    """The touched rows in each type and with gaps behind the rows: the sums as in the dense form, the gaps
+    and the rows behind the last one left alone (checked by _gradient, and the gaps here)."""
+    import torch
+    R = 77
+    ids = _tokens(T, R, 5, "few")
+    dt = _dt(("bf16", "f16", "f32")[(T + d) % 3])
+    dY = torch.randn(T, d, device="cuda", generator=torch.Generator("cuda").manual_seed(d)).to(dt)
+    ref, mag, n = TR.embed_bwd(ids, dY.double().cpu().numpy(), R, 0.75)
+    st, got, rows, buf = _gradient(ids, dY, R, 0.75, out=out, ld=ld, compact=True)
+    assert st == 0
+    np.testing.assert_array_equal(rows, np.flatnonzero(n))
+    tol = (n[:, None] + 2) * 2.0 ** -24 * mag
+    assert (np.abs(got - ref) <= tol * 1.01 + HALF[out] * np.abs(ref) + TINY[out]).all()
+    assert (buf[:, d:] == -5.0).all()
