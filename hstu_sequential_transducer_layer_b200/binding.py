@@ -548,7 +548,12 @@ def hstu_embed_bwd_rows(ids, dY, n_rows: int, row_ids, rows, n_unique, workspace
 class GradTensors:
     """A list of gradients laid out once for hstu_grad_norm: dicts with "grad"
     (contiguous, bf16, fp16 or fp32) and, where only the first rows of it count,
-    "n_rows" (int64 [1] on the device)."""
+    "n_rows" (int64 [1] on the device).
+
+    The list keeps the tensors and takes their addresses here, not at the
+    calls: it is for buffers that stay, whose contents change.  A gradient that
+    is allocated anew needs a new list; the old one goes on using the old
+    tensor."""
 
     def __init__(self, tensors: Sequence[Dict[str, object]]):
         self.tensors = [dict(t) for t in tensors]  # keeps the memory alive
@@ -583,7 +588,8 @@ class AdamWTensors(GradTensors):
     dicts with "param", "grad", "m", "v"; optional "master" (fp32), "copy_f16"
     (fp16), "weight_decay"; with 8-bit states "m" and "v" are uint8 or
     float8_e4m3fn and "m_scale", "v_scale" uint8 (state_scales() of the
-    parameter); for a table with a row gradient "row_ids" and "n_rows"."""
+    parameter); for a table with a row gradient "row_ids" and "n_rows".  As for
+    GradTensors, addresses are taken once."""
 
     def _fill(self, c, t) -> None:
         import torch

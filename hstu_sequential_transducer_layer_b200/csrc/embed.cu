@@ -155,19 +155,25 @@ struct LookupArgs {
 constexpr int kLookupUnroll = 4;
 constexpr int64_t kCheckMax = 65536;
 
-// Y[t] = scale * E[ids[t]].  Bandwidth-bound (19.7 us for 38,070 x 1024 bf16:
-// 78 MB written and the touched rows read, at 4.6 TB/s; only setting 78 MB to
-// zero takes 12.2; more loads ahead, places of rows in shared memory and other
-// numbers of blocks gave 18.9 to 26); a thread keeps one column group of 8 elements (1 where a row is
-// not a multiple of 8) and walks the tokens, 4 loads in flight, so that no index
-// is divided inside the loop.
+// Y[t] = scale * E[ids[t]].  38,070 x 1024 bf16 take 19.7 us: 78 MB written and
+// as many read through L2, 36 MB of both through DRAM, 4.6 TB/s in all, with
+// 54 % of the issue slots used (88 instructions per 8 elements, most of them ids
+// and addresses), so neither memory nor issue alone bounds it.  Only setting 78 MB
+// to zero takes 12.2; more loads ahead, places of rows in shared memory and other
+// numbers of blocks gave 18.9 to 26.  A thread keeps one column group of 8
+// elements (1 where a row is not a multiple of 8) and walks the tokens, 4 loads in
+// flight, so that no index is divided inside the loop.
 // Both types are compiled in: with a branch on the output's type per store the
 // kernel was bound by instructions (12.5 per element).  A dropped token's
-// loads are replaced by zeros.
+// loads are replaced by zeros.  (Some of the vector forms spill 4 bytes at their
+// register limit.)
 // A thread of one block cannot clear the status word before another one sets
 // it, so up to kCheckMax tokens block 0 copies nothing and validates all ids
-// itself (its 8 bytes per token are read while the others copy); beyond that
-// the word is cleared by a memset before the launch.
+// itself; beyond that the word is cleared by a memset before the launch, 1.5 to
+// 3 us.  Checking block against memset, bf16: 1,024 x 64 2.8 and 4.8 us;
+// 16,384 x 8 3.3 and 5.0; 16,384 x 1032 12.9 and 14.5; 38,070 x 1024 19.7 and 22.8;
+// 65,536 x 8 8.5 and 6.3; 65,536 x 1032 45 and 37: near the border the one block,
+// whose time grows with the tokens, is what the launch waits for.
 template <int DT, int OUT, bool VEC>
 __global__ void __launch_bounds__(256, DT == HSTU_FP32 || OUT == HSTU_FP32 ? 4 : 5)
     k_embed_lookup(const LookupArgs a) {

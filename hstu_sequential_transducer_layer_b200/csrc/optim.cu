@@ -724,7 +724,8 @@ DEVI bool next_block(const StepTensor& q, RowWalk& w, int* status, BlockAt& at) 
 // SMs, which cost 20 to 45 us of 184 on 42M parameters.
 //
 // Thread blocks of 128 threads per SM, measured on 42M parameters: fp32 states
-// 6 resident (80 registers) and 16 launched (218 us, 6.2 TB/s; 8 resident at 64
+// 6 resident (80 registers, at which the form for any types, kAny, spills 40
+// bytes) and 16 launched (218 us, 6.2 TB/s; 8 resident at 64
 // registers 235; no more launched than resident 228: the hardware's handing
 // out of thread blocks evens out what a fixed share does not).  8-bit states,
 // bound by instructions as much as by memory: with fp32 gradients and
@@ -1143,7 +1144,9 @@ hstu_status hstu_adamw_step(const hstu_adamw_args* args, const hstu_adamw_tensor
     const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), s);
     if (e != cudaSuccess) return cuda_status(e, "hstu_adamw_step");
   }
-  // one block at a time where more would leave warps without work
+  // One block at a time where more would leave warps without work.  One against kPerWarp at a
+  // time: 1M elements 6.4 and 7.0 us, 2M 10.0 and 9.3, 4M 15.5 and 16.7, 8M 26.5 and 27.3, 9.6M (the
+  // border) 31.0 and 31.0, 42M 187 and 141.
   const bool large = blocks >= (int64_t)num_sms() * 32 * kPerWarp * 2;
   return n_tensors <= kFewTensors ? adamw<kFewTensors>(h, tensors, n_tensors, fails, large, ws, s)
                                   : adamw<kMaxTensors>(h, tensors, n_tensors, fails, large, ws, s);

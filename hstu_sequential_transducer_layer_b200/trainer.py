@@ -23,10 +23,14 @@ class HSTUTrainer:
     W1 and W2 the update writes them too, so the next forward needs no
     conversion.  `table`: device [rows, d_model] (for hstu_sl_embed_ids: the
     content rows, then the action rows); at most `max_tokens` tokens per step.
-    Only the rows that a step's tokens touch are updated.
+    Only the rows that a step's tokens touch are updated.  A 16-bit table has an
+    fp32 master like the weights (4 bytes an element); a table that is to do
+    without one can be updated by hstu_adamw_step directly.
 
     The state is made on torch's current stream; a step on another stream has
-    to be ordered behind that (`stream.wait_stream`), as for its inputs."""
+    to be ordered behind that (`stream.wait_stream`), as for its inputs.  The step
+    number is counted on the host: a captured step() would replay its own (for
+    a graph, hstu_adamw_step takes the number from the device)."""
 
     def __init__(self, runner: HSTURunner, table=None, max_tokens: int = 0, state_bits: int = 32,
                  lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,

@@ -461,7 +461,11 @@ typedef struct {
   const void* grad;        /* of grad_dtype */
   void* param;             /* of param_dtype, updated */
   float* master;           /* optional fp32 copy of a 16-bit param: read and updated in its
-                            * place; param then receives the rounded result */
+                            * place; param then receives the rounded result.  Without one a
+                            * 16-bit param is rounded to nearest after every step, and what is
+                            * less than half a step of its type is lost: in bf16 a change below
+                            * |p| / 512 to |p| / 256, so weight decay as a rule, and updates of
+                            * the size of lr where |p| > 512 lr */
   void* copy_f16;          /* optional: receives the new (rounded) param as fp16, saturating at
                             * +-65504, as hstu_bf16_to_f16 does (W1_f16, W2_f16) */
   void* m;                 /* first moment: fp32, or e4m3 codes */
