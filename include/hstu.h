@@ -240,7 +240,9 @@ hstu_status hstu_layer_fwd_noalloc(const hstu_layer_desc* desc, int64_t B, int64
  * grads: host array [n_layers] of device pointers.  Workspace:
  * hstu_bwd_workspace_size() bytes, 256-byte aligned.  Asynchronous on
  * `stream`; device-detected errors (bad offsets or timestamps, a wait that
- * gave up) set the workspace's status word (hstu_read_status). */
+ * gave up) set the workspace's status word (hstu_read_status) and leave dX and
+ * gradients unwritten or partly written (hstu_grad_norm_after tells an
+ * optimizer step on the device). */
 typedef struct {
   float* dW1;        /* [F, d_model] */
   float* db1;        /* [F] */
